@@ -211,6 +211,41 @@ fa_status fa_rows_decode_static(const fa_rows_args* a, fa_stream_t stream);
 fa_status fa_rows_prefill(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream);
 
 /*
+ * Decode and prefill over one list per (slice, KV head): kv_rows [S, Hkv, L]
+ * and kv_len [S, Hkv] (or NULL), so the heads of a slice may read different
+ * rows (the lists that fa_kv_block_rows makes).  Everything else is as in
+ * fa_rows_decode / fa_rows_prefill, the workspace and its size included, with
+ * FA_MASK_NONE or FA_MASK_CAUSAL: a causal query i of KV head g sees positions
+ * j <= kv_len[s, g] - Nq + i of its head's list, so each list must end with the
+ * slice's Nq newest positions.  n_valid_hint counts the entries of all lists
+ * divided by Hkv.  fa_rows_validate takes these lists with S * Hkv slices.
+ * Sparse attention over selected blocks (the v100llm article, section 5, and
+ * the llama.cpp-v100 README's QSA attend to a selected subset of the context).
+ */
+fa_status fa_rows_decode_heads(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream);
+fa_status fa_rows_prefill_heads(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream);
+
+/*
+ * Attention weight received by each list entry, accumulated:
+ *   acc[s, g, j] = decay * acc[s, g, j] + sum over i and the heads h of group g
+ *                  of exp(scale * <q[s,i,h], K[row_j, g]> + mask - lse[s,i,h])
+ * for every list position j < n_s, where lse [S, Nq, Hq] is what fa_rows_decode
+ * or fa_rows_prefill wrote for the same arguments: each term is the softmax
+ * weight that call gave the entry.  Of a, the fields v, v_scale, out, out_dtype
+ * and lse are not read.  Terms that the mask, the causal limit or a padding
+ * entry removes are zero, and so are those of a query whose lse is minus
+ * infinity; positions at or past n_s keep their acc.  decay = 1 accumulates;
+ * decay = 0 overwrites (acc is not read).  With S * Nq = 0 nothing is done.
+ *   acc      [S, Hkv, L] fp32
+ *   pools    every kind of fa_rows_args, D <= 256 with 16-byte multiples per
+ *            (row, KV head); any mask kind; any Nq and Hq / Hkv
+ *   ws       256 bytes, zero-filled once (it holds the status word)
+ * The order of the sums is fixed: equal calls give equal bits.
+ */
+fa_status fa_rows_weights(const fa_rows_args* a, const float* lse, float decay, float* acc, void* ws, size_t ws_bytes,
+                          fa_stream_t stream);
+
+/*
  * Range check of the lists (section 1: negative = padding; anything else must
  * name a pool row).  d_status is a device int64[2] that this call overwrites:
  * [0] = number of entries with kv_rows >= n_pool_rows (within kv_len),
@@ -304,6 +339,89 @@ size_t fa_kv_sparse_rows_workspace_size(int32_t S, int32_t n_max);
 fa_status fa_kv_sparse_rows(const float* score, int32_t n_max, const int32_t* n_len, int32_t S, int32_t sinks,
                             int32_t recent, int32_t k, const int32_t* row_map, int32_t* kv_rows, int32_t list_len,
                             void* ws, size_t ws_bytes, fa_stream_t stream);
+
+/*
+ * Eviction from row lists by accumulated weight.  Of each slice's
+ * n = min(kv_len[s], list_len) entries (kv_len NULL: list_len), these are kept:
+ * list positions 0 .. sinks-1, positions n-recent .. n-1, and of the positions
+ * between them the k with the largest total, the sum of acc over the KV heads
+ * rounded once to fp32 (formed with at least 48 bits).  Ties go to the smaller
+ * position; a NaN total ranks below every number; padding entries (negative
+ * rows) are never kept.  A slice with no more entries than that keeps them all.
+ *   acc       [S, Hkv, list_len] fp32 (fa_rows_weights), kv_rows [S, list_len]
+ *   rows_out  [S, out_len] the kept entries' rows in list order, then -1
+ *   len_out   [S] how many were kept
+ *   acc_out   [S, Hkv, out_len] their acc, then 0: the accumulator that goes
+ *             with rows_out
+ *   kept      [S, out_len] their list positions, then -1; or NULL
+ *   freed     [S, list_len] the other entries' rows in list order, then -1; or
+ *             NULL.  These pool rows may be reused.
+ * out_len >= sinks + recent + k.  Outputs must overlap neither each other nor
+ * the inputs.  No workspace.
+ */
+fa_status fa_kv_evict(const float* acc, const int32_t* kv_rows, const int32_t* kv_len, int32_t S, int32_t Hkv,
+                      int32_t list_len, int32_t sinks, int32_t recent, int32_t k, float* acc_out, int32_t* rows_out,
+                      int32_t* len_out, int32_t out_len, int32_t* kept, int32_t* freed, fa_stream_t stream);
+
+/*
+ * Elementwise bounds of the keys of 64-row pages (the blocks of
+ * fa_kv_block_scores): for each listed page, kmin and kmax[page, g, d] over the
+ * page's first fill[i] rows (fill NULL: 64; clamped to 0 .. 64).  Exact for a
+ * 16-bit pool; for a quantised pool the bounds of code * scale rounded outward
+ * (down for kmin, up for kmax) to bound_dtype.  A NaN key makes its bounds
+ * NaN.  Pages with fill <= 0, and page ids below 0 or at or past
+ * n_pool_rows / 64, are skipped: their bounds are left as they were.  A page
+ * listed twice must have the same fill both times.
+ *   k, k_scale  the K pool as in fa_rows_args; n_pool_rows a multiple of 64
+ *   pages, fill [n_pages] int32
+ *   kmin, kmax  [n_pool_rows / 64, Hkv, D] FA_F16 or FA_BF16 (the pool's dtype
+ *               for a 16-bit pool)
+ * Called for the touched pages after an append.
+ */
+fa_status fa_kv_block_bounds(const void* k, fa_dtype kv_dtype, const uint16_t* k_scale, int64_t n_pool_rows,
+                             int32_t Hkv, int32_t D, const int32_t* pages, const int32_t* fill, int32_t n_pages,
+                             void* kmin, void* kmax, fa_dtype bound_dtype, fa_stream_t stream);
+
+/*
+ * Scores of a sequence's blocks for each query slice and KV head:
+ *   score[s, g, b] = max over the slice's queries i and the heads h of group g of
+ *                    sum_d max(q_d, 0) * kmax[page, g, d] + min(q_d, 0) * kmin[page, g, d],
+ * which no dot product of one of those queries with a key of the block exceeds
+ * (but for fp32 rounding).  Minus infinity for b >= ceil(seq_len[s] / 64) and
+ * for page ids below 0 or at or past n_pool_pages; NaN where a term is NaN.
+ *   q          [S, Nq, Hq, D] and the bounds in the same dtype, D in {64,128,256}
+ *   page_table [n_seq, max_pages] int32; slice s reads row slice_seq[s], or row s
+ *              when slice_seq is NULL (several slices of one sequence: prompt tiles).
+ *              A slice whose slice_seq is outside 0 .. n_seq-1 scores minus infinity.
+ *   seq_len    [S] int32: positions that slice s may see
+ *   score      [S, Hkv, max_pages] fp32
+ *   ws         256 bytes, zero-filled once (it holds the status word)
+ */
+fa_status fa_kv_block_scores(const void* q, fa_dtype q_dtype, int32_t S, int32_t Nq, int32_t Hq, int32_t Hkv, int32_t D,
+                             const void* kmin, const void* kmax, int64_t n_pool_pages, const int32_t* page_table,
+                             int32_t n_seq, int32_t max_pages, const int32_t* seq_len, const int32_t* slice_seq,
+                             float* score, void* ws, size_t ws_bytes, fa_stream_t stream);
+
+/*
+ * Row lists of the best blocks of each (slice, KV head).  Of the
+ * nb = ceil(min(seq_len[s], 64 * max_pages) / 64) blocks: the first
+ * sink_blocks, the last recent_blocks, and of those between them the k with
+ * the largest score (ties to the smaller block; NaN below every number); all
+ * when there are no more.  Their rows page * 64 + t are listed in position
+ * order, the sequence's last block up to seq_len.
+ *   score    [S, Hkv, max_pages] fp32 (fa_kv_block_scores)
+ *   kv_rows  [S, Hkv, list_len] int32, padded with -1; a block whose page id is
+ *            negative (or page * 64 + 63 past int32) is listed as -1 entries
+ *   kv_len   [S, Hkv] int32: entries listed
+ * list_len >= 64 * (sink_blocks + recent_blocks + k).  page_table, seq_len and
+ * slice_seq as in fa_kv_block_scores.  The lists feed fa_rows_decode_heads and
+ * fa_rows_prefill_heads (causal: with recent_blocks >= 1 + ceil(Nq / 64) every
+ * list ends with the slice's Nq newest positions).
+ */
+fa_status fa_kv_block_rows(const float* score, const int32_t* page_table, int32_t n_seq, int32_t max_pages,
+                           const int32_t* seq_len, const int32_t* slice_seq, int32_t S, int32_t Hkv,
+                           int32_t sink_blocks, int32_t recent_blocks, int32_t k, int32_t* kv_rows, int32_t* kv_len,
+                           int32_t list_len, fa_stream_t stream);
 
 /*
  * KV append for 16-bit pools: pool[dst_rows[i]] = x[i] for i < n_rows

@@ -31,3 +31,6 @@ from .kvcache import (  # noqa: F401
     e4m3_value, e4m3_encode, quantize_fp8, dequantize_fp8,
 )
 from .sparse import select_rows  # noqa: F401
+from .cache import (  # noqa: F401
+    attend_rows_heads, attention_weights, evict, round_outward, block_bounds, block_scores, block_rows,
+)

@@ -12,6 +12,7 @@ infinity); the result is exact attention over the listed rows.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,7 +23,8 @@ import torch
 __all__ = [
     "FaRowsError", "lib", "library_path", "fa_rows_args", "fa_rows_workspace_size", "fa_rows_workspace_init",
     "fa_rows_status", "fa_set_wait_limit_ns", "default_workspace", "FA_WS_WAIT_EXPIRED",
-    "fa_rows_decode", "fa_rows_prefill", "fa_rows_validate", "fa_kv_page_table_to_rows", "fa_kv_quantize_int8",
+    "fa_rows_decode", "fa_rows_prefill", "fa_rows_decode_heads", "fa_rows_prefill_heads", "fa_rows_weights",
+    "fa_kv_evict", "fa_kv_block_bounds", "fa_kv_block_scores", "fa_kv_block_rows", "fa_rows_validate", "fa_kv_page_table_to_rows", "fa_kv_quantize_int8",
     "fa_kv_dequantize_int8", "fa_kv_quantize_int4", "fa_kv_dequantize_int4", "fa_kv_quantize_fp8", "fa_kv_dequantize_fp8", "fa_kv_sparse_rows_workspace_size", "fa_kv_sparse_rows", "fa_kv_append", "fa_status_string", "fa_last_error", "fa_version",
     "FA_F16", "FA_BF16", "FA_F32", "FA_I8", "FA_I4", "FA_F8E4M3", "FA_MASK_NONE", "FA_MASK_DENSE", "FA_MASK_CAUSAL",
 ]
@@ -92,6 +94,16 @@ _SIGS = {
                                          ctypes.c_int32, _P, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "fa_kv_append": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                     ctypes.c_int64, _P]),
+    "fa_rows_decode_heads": (ctypes.c_int, [ctypes.POINTER(fa_rows_args), _P, ctypes.c_size_t, _P]),
+    "fa_rows_prefill_heads": (ctypes.c_int, [ctypes.POINTER(fa_rows_args), _P, ctypes.c_size_t, _P]),
+    "fa_rows_weights": (ctypes.c_int, [ctypes.POINTER(fa_rows_args), _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "fa_kv_evict": (ctypes.c_int, [_P, _P, _P] + [ctypes.c_int32] * 6 + [_P, _P, _P, ctypes.c_int32, _P, _P, _P]),
+    "fa_kv_block_bounds": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                          ctypes.c_int32, _P, _P, ctypes.c_int, _P]),
+    "fa_kv_block_scores": (ctypes.c_int, [_P, ctypes.c_int] + [ctypes.c_int32] * 5 + [_P, _P, ctypes.c_int64, _P,
+                                          ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "fa_kv_block_rows": (ctypes.c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P] + [ctypes.c_int32] * 5 +
+                         [_P, _P, ctypes.c_int32, _P]),
     "fa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fa_last_error": (ctypes.c_char_p, []),
     "fa_version": (ctypes.c_char_p, []),
@@ -189,22 +201,26 @@ def default_workspace(device=None, stream=None, is_prefill: bool = False) -> Opt
 
 
 def make_args(q, k, v, kv_rows, scale, *, kv_len=None, mask=None, causal=False, k_scale=None, v_scale=None,
-              out=None, lse=None, out_dtype=torch.float32, want_lse=False, n_valid_hint=0):
-    """Builds fa_rows_args from torch tensors; allocates ``out``/``lse`` if not given."""
+              out=None, lse=None, out_dtype=torch.float32, want_lse=False, n_valid_hint=0, head_lists=False):
+    """Builds fa_rows_args from torch tensors; allocates ``out``/``lse`` if not given.
+
+    head_lists: kv_rows is [S, Hkv, L] and kv_len [S, Hkv], one list per KV head.
+    """
     S, Nq, Hq, D = q.shape
     R, Hkv, Dk = k.shape
     packed = k.dtype == torch.uint8   # INT4 pool: two codes per byte
     if tuple(v.shape) != (R, Hkv, Dk) or Dk * (2 if packed else 1) != D:
         raise ValueError(f"k {tuple(k.shape)} / v {tuple(v.shape)} do not match q {tuple(q.shape)}")
-    if kv_rows.dtype != torch.int32 or kv_rows.dim() != 2 or kv_rows.shape[0] != S:
-        raise ValueError("kv_rows must be int32 [S, L]")
+    lists = (S, Hkv) if head_lists else (S,)
+    if kv_rows.dtype != torch.int32 or tuple(kv_rows.shape[:-1]) != lists:
+        raise ValueError("kv_rows must be int32 [S, Hkv, L]" if head_lists else "kv_rows must be int32 [S, L]")
     if k.dtype != v.dtype:
         raise ValueError("k and v must share a dtype")
     if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn) and (k_scale is None or v_scale is None):
         raise ValueError("a quantised pool needs k_scale and v_scale")
-    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (S,)):
-        raise ValueError("kv_len must be int32 [S]")
-    if mask is not None and (mask.dtype != torch.float32 or tuple(mask.shape) != (S, Nq, kv_rows.shape[1])):
+    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != lists):
+        raise ValueError("kv_len must be int32 [S, Hkv]" if head_lists else "kv_len must be int32 [S]")
+    if mask is not None and (mask.dtype != torch.float32 or tuple(mask.shape) != (S, Nq, kv_rows.shape[-1])):
         raise ValueError("mask must be float32 [S, Nq, L]")
     if out is None:
         out = torch.empty((S, Nq, Hq, D), dtype=out_dtype, device=q.device)
@@ -215,7 +231,7 @@ def make_args(q, k, v, kv_rows, scale, *, kv_len=None, mask=None, causal=False, 
     a.k, a.v, a.kv_dtype = _ptr(k), _ptr(v), _DT[k.dtype]
     a.k_scale, a.v_scale = _ptr(k_scale), _ptr(v_scale)
     a.n_pool_rows = R
-    a.kv_rows, a.list_len = _ptr(kv_rows), kv_rows.shape[1]
+    a.kv_rows, a.list_len = _ptr(kv_rows), kv_rows.shape[-1]
     a.kv_len = _ptr(kv_len)
     if mask is not None:
         a.mask_kind, a.mask = FA_MASK_DENSE, _ptr(mask)
@@ -289,6 +305,214 @@ def fa_rows_decode(q, k, v, kv_rows, scale, **kw):
 def fa_rows_prefill(q, k, v, kv_rows, scale, **kw):
     """Prefill (many query rows per slice), tensor-core path.  Same arguments as decode."""
     return _attend("fa_rows_prefill", True, q, k, v, kv_rows, scale, **kw)
+
+
+def fa_rows_decode_heads(q, k, v, kv_rows, scale, **kw):
+    """Decode over one list per (slice, KV head): kv_rows int32 [S, Hkv, L], kv_len int32 [S, Hkv].
+
+    Keyword args as fa_rows_decode, without mask; n_valid_hint is the entries of
+    all lists divided by Hkv.
+    """
+    _same_device(q.device, k, v, kv_rows, kw.get("kv_len"))
+    with _on(q.device):
+        return _attend("fa_rows_decode_heads", False, q, k, v, kv_rows, scale, head_lists=True, **kw)
+
+
+def fa_rows_prefill_heads(q, k, v, kv_rows, scale, **kw):
+    """Prefill over one list per (slice, KV head), as fa_rows_decode_heads; causal: each list
+    ends with the slice's Nq newest positions."""
+    _same_device(q.device, k, v, kv_rows, kw.get("kv_len"))
+    with _on(q.device):
+        return _attend("fa_rows_prefill_heads", True, q, k, v, kv_rows, scale, head_lists=True, **kw)
+
+
+def _status_ws(workspace, device, sh, need: int = 256):
+    """(pointer, bytes, tensor) of the caller's workspace or the binding's own one for calls that
+    need the status block alone."""
+    if workspace is not None:
+        return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+    wsobj = _default_ws(device, sh, True)
+    wptr, wbytes = wsobj.get(need, device, sh)
+    return wptr, wbytes, wsobj.buf
+
+
+def _raise_expired(entry: str, wtensor, stream):
+    word = fa_rows_status(wtensor, clear=True, stream=stream)
+    if word & FA_WS_WAIT_EXPIRED:
+        raise FaRowsError(FA_ERR_WAIT_EXPIRED, f"{entry}: a pipeline wait ran out; the outputs are invalid")
+
+
+def _on(device):
+    """Context that makes ``device`` the current one (nothing to do when it is)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors must share one device ({t.device} and {device})")
+
+
+def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, kv_len=None, mask=None, causal=False,
+                    k_scale=None, workspace=None, stream=None, check_status=False) -> torch.Tensor:
+    """acc [S, Hkv, L] += the softmax weight each list entry received from the attention call that
+    returned ``lse`` for the same arguments (acc None: a new zero accumulator; decay scales the old acc)."""
+    S, Nq, Hq, D = q.shape
+    R, Hkv, Dk = k.shape
+    if Dk * (2 if k.dtype == torch.uint8 else 1) != D:
+        raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
+    if kv_rows.dtype != torch.int32 or kv_rows.dim() != 2 or kv_rows.shape[0] != S:
+        raise ValueError("kv_rows must be int32 [S, L]")
+    L = kv_rows.shape[1]
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (S, Nq, Hq):
+        raise ValueError("lse must be float32 [S, Nq, Hq]")
+    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (S,)):
+        raise ValueError("kv_len must be int32 [S]")
+    if mask is not None and (mask.dtype != torch.float32 or tuple(mask.shape) != (S, Nq, L)):
+        raise ValueError("mask must be float32 [S, Nq, L]")
+    if acc is None:
+        acc = torch.zeros((S, Hkv, L), dtype=torch.float32, device=q.device)
+    elif acc.dtype != torch.float32 or tuple(acc.shape) != (S, Hkv, L):
+        raise ValueError("acc must be float32 [S, Hkv, L]")
+    _same_device(q.device, k, kv_rows, lse, acc, kv_len, mask, k_scale, workspace)
+    a = fa_rows_args()
+    a.q, a.q_dtype = _ptr(q), _DT[q.dtype]
+    a.k, a.kv_dtype, a.k_scale = _ptr(k), _DT[k.dtype], _ptr(k_scale)
+    a.n_pool_rows = R
+    a.kv_rows, a.list_len, a.kv_len = _ptr(kv_rows), L, _ptr(kv_len)
+    a.mask_kind = FA_MASK_DENSE if mask is not None else FA_MASK_CAUSAL if causal else FA_MASK_NONE
+    a.mask = _ptr(mask)
+    a.scale = float(scale)
+    a.S, a.Nq, a.Hq, a.Hkv, a.D = S, Nq, Hq, Hkv, D
+    with _on(q.device):
+        sh = _stream(stream, q.device)
+        wptr, wbytes, wtensor = _status_ws(workspace, q.device, sh)
+        _check(lib().fa_rows_weights(ctypes.byref(a), _ptr(lse), float(decay), _ptr(acc), wptr, wbytes, sh))
+    if check_status:
+        _raise_expired("fa_rows_weights", wtensor, stream)
+    return acc
+
+
+def fa_kv_evict(acc, kv_rows, kv_len, sinks: int, recent: int, k: int, *, out_len: Optional[int] = None, acc_out=None,
+                rows_out=None, len_out=None, kept=None, freed=None, stream=None):
+    """Keeps the sinks, the recent entries and the k heaviest of the others of each list.
+
+    Returns (rows [S, out_len], length [S], acc [S, Hkv, out_len], kept positions [S, out_len],
+    freed rows [S, L]); -1 (acc: 0) past the end.  out_len None: sinks + recent + k.
+    """
+    if acc.dtype != torch.float32 or acc.dim() != 3:
+        raise ValueError("acc must be float32 [S, Hkv, L]")
+    S, Hkv, L = acc.shape
+    if kv_rows.dtype != torch.int32 or tuple(kv_rows.shape) != (S, L):
+        raise ValueError("kv_rows must be int32 [S, L]")
+    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (S,)):
+        raise ValueError("kv_len must be int32 [S]")
+    n = int(out_len) if out_len is not None else int(sinks) + int(recent) + int(k)
+    dev = acc.device
+
+    def dest(t, shape, dtype, name):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {dtype} {shape}")
+        return t
+
+    rows_out = dest(rows_out, (S, n), torch.int32, "rows_out")
+    len_out = dest(len_out, (S,), torch.int32, "len_out")
+    acc_out = dest(acc_out, (S, Hkv, n), torch.float32, "acc_out")
+    kept = dest(kept, (S, n), torch.int32, "kept")
+    freed = dest(freed, (S, L), torch.int32, "freed")
+    _same_device(dev, kv_rows, kv_len, rows_out, len_out, acc_out, kept, freed)
+    with _on(dev):
+        _check(lib().fa_kv_evict(_ptr(acc), _ptr(kv_rows), _ptr(kv_len), S, Hkv, L, int(sinks), int(recent), int(k),
+                                 _ptr(acc_out), _ptr(rows_out), _ptr(len_out), n, _ptr(kept), _ptr(freed),
+                                 _stream(stream, dev)))
+    return rows_out, len_out, acc_out, kept, freed
+
+
+def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None):
+    """Updates kmin, kmax [R/64, Hkv, D] with the elementwise key bounds of the listed 64-row pages
+    (the first fill[i] rows of each; fill None: 64).  Returns (kmin, kmax)."""
+    R, Hkv, Dk = k.shape
+    D = Dk * (2 if k.dtype == torch.uint8 else 1)
+    if kmin.dtype != kmax.dtype or tuple(kmin.shape) != (R // 64, Hkv, D) or tuple(kmax.shape) != (R // 64, Hkv, D):
+        raise ValueError(f"kmin and kmax must be [R/64, Hkv, D] = {(R // 64, Hkv, D)} of one dtype")
+    for t, name in ((pages, "pages"), (fill, "fill")):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(pages.shape) or t.dim() != 1):
+            raise ValueError(f"{name} must be int32 [n_pages]")
+    if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+        if k_scale is None:
+            raise ValueError("a quantised pool needs k_scale")
+    _same_device(k.device, pages, fill, kmin, kmax, k_scale)
+    with _on(k.device):
+        _check(lib().fa_kv_block_bounds(_ptr(k), _DT[k.dtype], _ptr(k_scale), R, Hkv, D, _ptr(pages), _ptr(fill),
+                                        pages.shape[0], _ptr(kmin), _ptr(kmax), _DT[kmin.dtype],
+                                        _stream(stream, k.device)))
+    return kmin, kmax
+
+
+def _check_pages(S, page_table, seq_len, slice_seq):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [n_seq, max_pages]")
+    if seq_len.dtype != torch.int32 or tuple(seq_len.shape) != (S,):
+        raise ValueError("seq_len must be int32 [S]")
+    if slice_seq is not None and (slice_seq.dtype != torch.int32 or tuple(slice_seq.shape) != (S,)):
+        raise ValueError("slice_seq must be int32 [S]")
+
+
+def fa_kv_block_scores(q, kmin, kmax, page_table, seq_len, *, slice_seq=None, out=None, workspace=None, stream=None,
+                       check_status=False) -> torch.Tensor:
+    """Upper bounds [S, Hkv, max_pages] of the dot products of each slice's queries with the keys of
+    each block of its sequence (page_table row slice_seq[s], or s)."""
+    S, Nq, Hq, D = q.shape
+    P, Hkv, Dk = kmin.shape
+    if Dk != D or kmin.shape != kmax.shape or kmin.dtype != q.dtype or kmax.dtype != q.dtype:
+        raise ValueError("kmin and kmax must be [pages, Hkv, D] of q's dtype")
+    _check_pages(S, page_table, seq_len, slice_seq)
+    n_seq, max_pages = page_table.shape
+    if out is None:
+        out = torch.empty((S, Hkv, max_pages), dtype=torch.float32, device=q.device)
+    elif out.dtype != torch.float32 or tuple(out.shape) != (S, Hkv, max_pages):
+        raise ValueError("out must be float32 [S, Hkv, max_pages]")
+    _same_device(q.device, kmin, kmax, page_table, seq_len, slice_seq, out, workspace)
+    with _on(q.device):
+        sh = _stream(stream, q.device)
+        wptr, wbytes, wtensor = _status_ws(workspace, q.device, sh)
+        _check(lib().fa_kv_block_scores(_ptr(q), _DT[q.dtype], S, Nq, Hq, Hkv, D, _ptr(kmin), _ptr(kmax), P,
+                                        _ptr(page_table), n_seq, max_pages, _ptr(seq_len), _ptr(slice_seq), _ptr(out),
+                                        wptr, wbytes, sh))
+    if check_status:
+        _raise_expired("fa_kv_block_scores", wtensor, stream)
+    return out
+
+
+def fa_kv_block_rows(score, page_table, seq_len, sink_blocks: int, recent_blocks: int, k: int, *, slice_seq=None,
+                     list_len: Optional[int] = None, out=None, out_len=None, stream=None):
+    """Row lists [S, Hkv, list_len] and lengths [S, Hkv] of the first sink_blocks, the last
+    recent_blocks and the k best-scored other blocks (list_len None: 64 per block)."""
+    if score.dtype != torch.float32 or score.dim() != 3:
+        raise ValueError("score must be float32 [S, Hkv, max_pages]")
+    S, Hkv, max_pages = score.shape
+    _check_pages(S, page_table, seq_len, slice_seq)
+    if page_table.shape[1] != max_pages:
+        raise ValueError("page_table and score must have the same max_pages")
+    L = 64 * (int(sink_blocks) + int(recent_blocks) + int(k)) if list_len is None else int(list_len)
+    if out is None:
+        out = torch.empty((S, Hkv, L), dtype=torch.int32, device=score.device)
+    elif out.dtype != torch.int32 or tuple(out.shape) != (S, Hkv, L):
+        raise ValueError("out must be int32 [S, Hkv, list_len]")
+    if out_len is None:
+        out_len = torch.empty((S, Hkv), dtype=torch.int32, device=score.device)
+    elif out_len.dtype != torch.int32 or tuple(out_len.shape) != (S, Hkv):
+        raise ValueError("out_len must be int32 [S, Hkv]")
+    _same_device(score.device, page_table, seq_len, slice_seq, out, out_len)
+    with _on(score.device):
+        _check(lib().fa_kv_block_rows(_ptr(score), _ptr(page_table), page_table.shape[0], max_pages, _ptr(seq_len),
+                                      _ptr(slice_seq), S, Hkv, int(sink_blocks), int(recent_blocks), int(k), _ptr(out),
+                                      _ptr(out_len), L, _stream(stream, score.device)))
+    return out, out_len
 
 
 def fa_rows_validate(kv_rows: torch.Tensor, n_pool_rows: int, kv_len=None, stream=None) -> Tuple[int, int]:

@@ -7,8 +7,12 @@
 
 #include <atomic>
 
+#include "blocks.cuh"
 #include "decode.cuh"
+#include "evict.cuh"
 #include "fa_internal.cuh"
+#include "kvread.cuh"
+#include "weights.cuh"
 
 namespace {
 
@@ -102,6 +106,18 @@ fa_status check_common(const fa_rows_args* a) {
   return FA_OK;
 }
 
+// One list per (slice, KV head): a dense mask follows the positions of one
+// list per slice, so it has no meaning here.
+fa_status check_head_lists(const fa_rows_args* a) {
+  g_err[0] = 0;
+  if (!a) return fail(FA_ERR_INVALID_ARG, "args is NULL");
+  if (a->mask_kind == FA_MASK_DENSE)
+    return fail(FA_ERR_UNSUPPORTED, "lists per KV head take FA_MASK_NONE or FA_MASK_CAUSAL");
+  if (a->S > 0 && a->Hkv > 0 && (long long)a->S * a->Hkv > 0x7fffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "S * Hkv lists must fit int32");
+  return FA_OK;
+}
+
 struct DecodePlan {
   bool tc = false;   // tensor-core kernel (either of the two below)
   bool tcq = false;  // the quantised-pool tensor-core kernel
@@ -112,6 +128,17 @@ struct DecodePlan {
 };
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+constexpr int kMaxGrid = 65535;   // blocks in the y and z dimensions of a launch
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& a, const Span& b) {
+  const char *x = static_cast<const char*>(a.p), *y = static_cast<const char*>(b.p);
+  return x && y && a.n && b.n && x < y + b.n && y < x + a.n;
+}
 
 constexpr int kMaxSplits = far::kDecodeMaxSplits;
 constexpr long long kMergeMaxFloats = 32 * 1024;   // partial floats one merging CTA reads, at most (16-bit tc decode)
@@ -320,7 +347,7 @@ fa_status fa_set_wait_limit_ns(uint64_t limit_ns) {
   return FA_OK;
 }
 
-fa_status fa_rows_decode(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+static fa_status decode_call(const fa_rows_args* a, bool head_lists, void* ws, size_t ws_bytes, fa_stream_t stream) {
   g_err[0] = 0;
   fa_status st = check_common(a);
   if (st != FA_OK) return st;
@@ -367,6 +394,7 @@ fa_status fa_rows_decode(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_st
   p.qscale = a->scale * far::kLog2e;
   p.wait_ns = wait_limit();
   p.merge_kernel = pl.merge_kernel ? 1 : 0;
+  p.head_lists = head_lists ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
   const int kind = kv_kind(a->kv_dtype);
@@ -384,7 +412,16 @@ fa_status fa_rows_decode(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_st
   return e == cudaSuccess ? FA_OK : cuda_fail(e, "decode launch");
 }
 
-fa_status fa_rows_prefill(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+fa_status fa_rows_decode(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+  return decode_call(a, false, ws, ws_bytes, stream);
+}
+
+fa_status fa_rows_decode_heads(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+  const fa_status st = check_head_lists(a);
+  return st == FA_OK ? decode_call(a, true, ws, ws_bytes, stream) : st;
+}
+
+static fa_status prefill_call(const fa_rows_args* a, bool head_lists, void* ws, size_t ws_bytes, fa_stream_t stream) {
   g_err[0] = 0;
   fa_status st = check_common(a);
   if (st != FA_OK) return st;
@@ -422,8 +459,18 @@ fa_status fa_rows_prefill(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_s
   p.qscale = a->scale * far::kLog2e;
   p.err = static_cast<unsigned int*>(ws);   // the status word
   p.wait_ns = wait_limit();
+  p.head_lists = head_lists ? 1 : 0;
   cudaError_t e = far::prefill_launch(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, "prefill launch");
+}
+
+fa_status fa_rows_prefill(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+  return prefill_call(a, false, ws, ws_bytes, stream);
+}
+
+fa_status fa_rows_prefill_heads(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_stream_t stream) {
+  const fa_status st = check_head_lists(a);
+  return st == FA_OK ? prefill_call(a, true, ws, ws_bytes, stream) : st;
 }
 
 fa_status fa_rows_validate(const fa_rows_args* a, int64_t* d_status, fa_stream_t stream) {
@@ -577,6 +624,230 @@ fa_status fa_kv_append(const void* x, fa_dtype dtype, int64_t n_rows, int32_t Hk
   cudaError_t e = far::launch_kv_append(x, n_rows, (int)row_bytes, dst_rows, pool, n_pool_rows,
                                         reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, "append launch");
+}
+
+fa_status fa_rows_weights(const fa_rows_args* a, const float* lse, float decay, float* acc, void* ws, size_t ws_bytes,
+                          fa_stream_t stream) {
+  g_err[0] = 0;
+  if (!a) return fail(FA_ERR_INVALID_ARG, "args is NULL");
+  fa_rows_args c = *a;   // the call reads K alone and writes acc: v, out and a->lse do not take part
+  c.v = c.k;
+  c.v_scale = c.k_scale;
+  c.out = acc;
+  c.out_dtype = FA_F32;
+  c.lse = nullptr;
+  const fa_status st = check_common(&c);
+  if (st != FA_OK) return st;
+  const int kind = kv_kind(c.kv_dtype);
+  if (c.D > 256 || far::kv_row_bytes(kind, c.D) % 16 != 0)
+    return fail(FA_ERR_UNSUPPORTED, "weights need D <= 256 and 16-byte multiples per (row, KV head); got D=%d", c.D);
+  if (c.S > kMaxGrid || c.Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices and KV heads", kMaxGrid);
+  if ((long long)c.S * c.Nq == 0 || c.list_len == 0) return FA_OK;
+  if (!lse || !aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be the fp32 [S, Nq, Hq] of the attention call");
+  if (!isfinite(decay)) return fail(FA_ERR_INVALID_ARG, "decay must be finite");
+  if (!ws || ws_bytes < kPrefillWorkspace || !aligned(ws, 16))
+    return fail(FA_ERR_WORKSPACE, "weights need a zero-initialised workspace of %zu bytes, 16-byte aligned (it holds "
+                                  "the status word)", kPrefillWorkspace);
+  far::WeightsParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = c.q;
+  p.k = c.k;
+  p.k_scale = c.k_scale;
+  p.kv_rows = c.kv_rows;
+  p.kv_len = c.kv_len;
+  p.mask = c.mask;
+  p.lse = lse;
+  p.acc = acc;
+  p.R = c.n_pool_rows;
+  p.S = c.S;
+  p.Nq = c.Nq;
+  p.Hq = c.Hq;
+  p.Hkv = c.Hkv;
+  p.L = c.list_len;
+  p.G = c.Hq / c.Hkv;
+  p.D = c.D;
+  p.kind = kind;
+  p.q_bf16 = c.q_dtype == FA_BF16;
+  p.mask_kind = c.mask_kind;
+  p.scale = c.scale;
+  p.decay = decay;
+  p.err = static_cast<unsigned int*>(ws);   // the status word
+  p.wait_ns = wait_limit();
+  cudaError_t e = far::weights_launch(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "weights launch");
+}
+
+fa_status fa_kv_evict(const float* acc, const int32_t* kv_rows, const int32_t* kv_len, int32_t S, int32_t Hkv,
+                      int32_t list_len, int32_t sinks, int32_t recent, int32_t k, float* acc_out, int32_t* rows_out,
+                      int32_t* len_out, int32_t out_len, int32_t* kept, int32_t* freed, fa_stream_t stream) {
+  g_err[0] = 0;
+  if (S < 0 || Hkv <= 0 || list_len < 0 || sinks < 0 || recent < 0 || k < 0 || out_len < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size (S=%d Hkv=%d L=%d sinks=%d recent=%d k=%d out_len=%d)", S, Hkv,
+                list_len, sinks, recent, k, out_len);
+  if ((long long)sinks + recent + k > out_len)
+    return fail(FA_ERR_INVALID_ARG, "out_len %d < sinks + recent + k = %lld", out_len, (long long)sinks + recent + k);
+  if (S > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices", kMaxGrid);
+  if (list_len > (1 << 30) || out_len > (1 << 30)) return fail(FA_ERR_UNSUPPORTED, "at most 2^30 list entries");
+  if (S == 0) return FA_OK;
+  if (!len_out || (list_len > 0 && (!acc || !kv_rows)) || (out_len > 0 && (!acc_out || !rows_out)))
+    return fail(FA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(acc, 4) || !aligned(kv_rows, 4) || !aligned(kv_len, 4) || !aligned(acc_out, 4) || !aligned(rows_out, 4) ||
+      !aligned(len_out, 4) || !aligned(kept, 4) || !aligned(freed, 4))
+    return fail(FA_ERR_INVALID_ARG, "tensors must be 4-byte aligned");
+  // every output is written while inputs are still read
+  const size_t nl = (size_t)S * list_len * 4, no = (size_t)S * out_len * 4;
+  const Span in[3] = {{acc, nl * Hkv}, {kv_rows, nl}, {kv_len, (size_t)S * 4}};
+  const Span out[5] = {{acc_out, no * Hkv}, {rows_out, no}, {len_out, (size_t)S * 4}, {kept, no}, {freed, nl}};
+  for (int i = 0; i < 5; ++i) {
+    for (const Span& x : in)
+      if (overlap(out[i], x)) return fail(FA_ERR_INVALID_ARG, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return fail(FA_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  far::EvictParams p;
+  memset(&p, 0, sizeof(p));
+  p.acc = acc;
+  p.kv_rows = kv_rows;
+  p.kv_len = kv_len;
+  p.acc_out = acc_out;
+  p.rows_out = rows_out;
+  p.len_out = len_out;
+  p.kept = kept;
+  p.freed = freed;
+  p.S = S;
+  p.Hkv = Hkv;
+  p.L = list_len;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.k = k;
+  p.out_len = out_len;
+  cudaError_t e = far::evict_launch(p, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "evict launch");
+}
+
+fa_status fa_kv_block_bounds(const void* k, fa_dtype kv_dtype, const uint16_t* k_scale, int64_t n_pool_rows,
+                             int32_t Hkv, int32_t D, const int32_t* pages, const int32_t* fill, int32_t n_pages,
+                             void* kmin, void* kmax, fa_dtype bound_dtype, fa_stream_t stream) {
+  g_err[0] = 0;
+  const int kind = kv_kind(kv_dtype);
+  if (kind < 0) return fail(FA_ERR_UNSUPPORTED, "kv dtype must be f16, bf16, i8, i4 or f8e4m3");
+  if (bound_dtype != FA_F16 && bound_dtype != FA_BF16) return fail(FA_ERR_UNSUPPORTED, "bounds are f16 or bf16");
+  const bool quant = kind == far::KV_I8 || kind == far::KV_I4 || kind == far::KV_F8;
+  if (!quant && bound_dtype != kv_dtype) return fail(FA_ERR_UNSUPPORTED, "bounds of a 16-bit pool have its dtype");
+  if (n_pool_rows < 0 || Hkv <= 0 || D <= 0 || n_pages < 0)
+    return fail(FA_ERR_INVALID_ARG, "bad sizes (R=%lld Hkv=%d D=%d n_pages=%d)", (long long)n_pool_rows, Hkv, D, n_pages);
+  if (n_pool_rows % far::kPage != 0 || n_pool_rows > 0x7fffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "pool rows must be a multiple of 64 and fit int32");
+  if (D > 256 || (kind == far::KV_I4 && D % 32 != 0) || far::kv_row_bytes(kind, D) % 16 != 0)
+    return fail(FA_ERR_UNSUPPORTED, "bounds need D <= 256 and 16-byte multiples per (row, KV head); got D=%d", D);
+  if (Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d KV heads", kMaxGrid);
+  if (n_pages == 0) return FA_OK;
+  if (!k || !pages || !kmin || !kmax || (quant && !k_scale)) return fail(FA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(k, 16) || !aligned(kmin, 16) || !aligned(kmax, 16) || !aligned(pages, 4) || !aligned(fill, 4) ||
+      !aligned(k_scale, 4))
+    return fail(FA_ERR_INVALID_ARG, "k, kmin and kmax need 16-byte alignment, other tensors 4-byte alignment");
+  far::BoundsParams p;
+  memset(&p, 0, sizeof(p));
+  p.k = k;
+  p.k_scale = quant ? k_scale : nullptr;
+  p.pages = pages;
+  p.fill = fill;
+  p.kmin = kmin;
+  p.kmax = kmax;
+  p.n_pool_pages = n_pool_rows / far::kPage;
+  p.n_pages = n_pages;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.kind = kind;
+  p.out_bf16 = bound_dtype == FA_BF16;
+  cudaError_t e = far::bounds_launch(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "block bounds launch");
+}
+
+fa_status fa_kv_block_scores(const void* q, fa_dtype q_dtype, int32_t S, int32_t Nq, int32_t Hq, int32_t Hkv, int32_t D,
+                             const void* kmin, const void* kmax, int64_t n_pool_pages, const int32_t* page_table,
+                             int32_t n_seq, int32_t max_pages, const int32_t* seq_len, const int32_t* slice_seq,
+                             float* score, void* ws, size_t ws_bytes, fa_stream_t stream) {
+  g_err[0] = 0;
+  if (q_dtype != FA_F16 && q_dtype != FA_BF16) return fail(FA_ERR_UNSUPPORTED, "q and the bounds are f16 or bf16");
+  if (S < 0 || Nq < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || n_seq < 0 || max_pages < 0 || n_pool_pages < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative or zero size (S=%d Nq=%d Hq=%d Hkv=%d D=%d)", S, Nq, Hq, Hkv, D);
+  if (Hq % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+  if (D != 64 && D != 128 && D != 256) return fail(FA_ERR_UNSUPPORTED, "block scores are built for D in {64,128,256}");
+  if (n_pool_pages > 0x7fffffffLL) return fail(FA_ERR_UNSUPPORTED, "pool pages must fit int32");
+  if (S > kMaxGrid || Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices and KV heads", kMaxGrid);
+  if (!slice_seq && S > n_seq) return fail(FA_ERR_INVALID_ARG, "%d slices need as many page-table rows (got %d)", S, n_seq);
+  if ((long long)max_pages * far::kPage > 0x7fffffffLL) return fail(FA_ERR_INVALID_ARG, "max_pages*64 overflows int32");
+  if ((long long)S * Nq == 0 || max_pages == 0) return FA_OK;
+  if (!q || !kmin || !kmax || !page_table || !seq_len || !score) return fail(FA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(kmin, 16) || !aligned(kmax, 16) || !aligned(page_table, 4) || !aligned(seq_len, 4) ||
+      !aligned(slice_seq, 4) || !aligned(score, 4))
+    return fail(FA_ERR_INVALID_ARG, "q, kmin and kmax need 16-byte alignment, other tensors 4-byte alignment");
+  if (!ws || ws_bytes < kPrefillWorkspace || !aligned(ws, 16))
+    return fail(FA_ERR_WORKSPACE, "block scores need a zero-initialised workspace of %zu bytes, 16-byte aligned (it "
+                                  "holds the status word)", kPrefillWorkspace);
+  far::ScoresParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.kmin = kmin;
+  p.kmax = kmax;
+  p.page_table = page_table;
+  p.seq_len = seq_len;
+  p.slice_seq = slice_seq;
+  p.score = score;
+  p.n_pool_pages = n_pool_pages;
+  p.S = S;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.D = D;
+  p.max_pages = max_pages;
+  p.n_seq = n_seq;
+  p.q_bf16 = q_dtype == FA_BF16;
+  p.err = static_cast<unsigned int*>(ws);   // the status word
+  p.wait_ns = wait_limit();
+  cudaError_t e = far::scores_launch(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "block scores launch");
+}
+
+fa_status fa_kv_block_rows(const float* score, const int32_t* page_table, int32_t n_seq, int32_t max_pages,
+                           const int32_t* seq_len, const int32_t* slice_seq, int32_t S, int32_t Hkv,
+                           int32_t sink_blocks, int32_t recent_blocks, int32_t k, int32_t* kv_rows, int32_t* kv_len,
+                           int32_t list_len, fa_stream_t stream) {
+  g_err[0] = 0;
+  if (S < 0 || Hkv <= 0 || n_seq < 0 || max_pages < 0 || sink_blocks < 0 || recent_blocks < 0 || k < 0 || list_len < 0)
+    return fail(FA_ERR_INVALID_ARG, "negative size");
+  if (((long long)sink_blocks + recent_blocks + k) * far::kPage > list_len)
+    return fail(FA_ERR_INVALID_ARG, "list_len %d < 64 * (sink_blocks + recent_blocks + k) = %lld", list_len,
+                ((long long)sink_blocks + recent_blocks + k) * far::kPage);
+  if (S > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices", kMaxGrid);
+  if (!slice_seq && S > n_seq) return fail(FA_ERR_INVALID_ARG, "%d slices need as many page-table rows (got %d)", S, n_seq);
+  if ((long long)max_pages * far::kPage > 0x7fffffffLL) return fail(FA_ERR_INVALID_ARG, "max_pages*64 overflows int32");
+  if (S == 0) return FA_OK;
+  if (!seq_len || !kv_len || (max_pages > 0 && (!score || !page_table)) || (list_len > 0 && !kv_rows))
+    return fail(FA_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(score, 4) || !aligned(page_table, 4) || !aligned(seq_len, 4) || !aligned(slice_seq, 4) ||
+      !aligned(kv_rows, 4) || !aligned(kv_len, 4))
+    return fail(FA_ERR_INVALID_ARG, "tensors must be 4-byte aligned");
+  far::BlockRowsParams p;
+  memset(&p, 0, sizeof(p));
+  p.score = score;
+  p.page_table = page_table;
+  p.seq_len = seq_len;
+  p.slice_seq = slice_seq;
+  p.kv_rows = kv_rows;
+  p.kv_len = kv_len;
+  p.S = S;
+  p.Hkv = Hkv;
+  p.max_pages = max_pages;
+  p.n_seq = n_seq;
+  p.sinks = sink_blocks;
+  p.recent = recent_blocks;
+  p.k = k;
+  p.list_len = list_len;
+  cudaError_t e = far::block_rows_launch(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "block rows launch");
 }
 
 }  // extern "C"

@@ -165,12 +165,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32) fa_rows_decode_kernel(const
   const int split = blockIdx.x, g = blockIdx.y, s = blockIdx.z;
   const int G = p.G;
   int n_s = p.L;
-  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + s), 0), p.L);
+  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + list_of(p, s, g)), 0), p.L);
   const int j0 = split * p.chunk;
   const int cnt = max(min(j0 + p.chunk, n_s) - j0, 0);
 
   // ---- stage this item's row indices (out-of-range rows count as padding)
-  const int32_t* rows_g = p.kv_rows + (size_t)s * p.L + j0;
+  const int32_t* rows_g = p.kv_rows + list_of(p, s, g) * p.L + j0;
   for (int t = threadIdx.x; t < cnt; t += NW * 32) {
     const int r = __ldg(rows_g + t);
     idx_s[t] = (r >= 0 && (long long)r < p.R) ? r : -1;

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
   const int G = p.G, QV = p.QV;
   const bool bf16 = p.q_bf16 != 0;
   int n_s = p.L;
-  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + s), 0), p.L);
+  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + list_of(p, s, g)), 0), p.L);
   // splits past the sequence's last entry do nothing and are not merged; a
   // sequence that fits one split writes its result directly
   const int ns_unit = n_s > 0 && p.chunk > 0 ? (n_s + p.chunk - 1) / p.chunk : 1;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
   const int j0 = split * p.chunk;
   const int cnt = max(min(j0 + p.chunk, n_s) - j0, 0);
   const int T = (cnt + BN - 1) / BN;
-  const int32_t* rows_g = p.kv_rows + (size_t)s * p.L + j0;
+  const int32_t* rows_g = p.kv_rows + list_of(p, s, g) * p.L + j0;
   const size_t unit = (size_t)s * p.Hkv + g;
 
   if (threadIdx.x == 0) {

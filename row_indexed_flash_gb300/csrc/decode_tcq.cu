@@ -272,7 +272,7 @@ __global__ void __maxnreg__((DqShape<QVP, KQ>::MAXREG))
   const int G = p.G, QV = p.QV;
   const bool q_bf16 = p.q_bf16 != 0;
   int n_s = p.L;
-  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + s), 0), p.L);
+  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + list_of(p, s, g)), 0), p.L);
   // splits past the sequence's last entry do nothing and are not merged; a
   // sequence that fits one split writes its result directly
   const int ns_unit = n_s > 0 && p.chunk > 0 ? (n_s + p.chunk - 1) / p.chunk : 1;
@@ -281,7 +281,7 @@ __global__ void __maxnreg__((DqShape<QVP, KQ>::MAXREG))
   const int j0 = split * p.chunk;
   const int cnt = max(min(j0 + p.chunk, n_s) - j0, 0);
   const int T = (cnt + BN - 1) / BN;
-  const int32_t* rows_g = p.kv_rows + (size_t)s * p.L + j0;
+  const int32_t* rows_g = p.kv_rows + list_of(p, s, g) * p.L + j0;
   const size_t unit = (size_t)s * p.Hkv + g;
   // List loads run tiles ahead of their use: each reads a clamped (always
   // valid) position and returns the raw entry, and the range test is applied

@@ -60,6 +60,7 @@ struct DecodeParams {
   float qscale;             // scale * log2(e), folded into Q
   unsigned long long wait_ns;   // limit of a pipeline wait (tensor-core kernels)
   int merge_kernel;         // 1: the splits are merged by decode_merge_launch after the decode, not in it
+  int head_lists;           // 1: one row list (and length) per (slice, KV head), else one per slice
 };
 
 struct DecodeConfig {
@@ -115,6 +116,7 @@ struct PrefillParams {
   float qscale;         // scale * log2(e)
   unsigned int* err;    // the workspace status word: FA_WS_WAIT_EXPIRED is or-ed in when a wait expires
   unsigned long long wait_ns;   // limit of a pipeline wait
+  int head_lists;       // 1: one row list (and length) per (slice, KV head), else one per slice
 };
 cudaError_t prefill_launch(const PrefillParams& p, cudaStream_t st);
 bool prefill_supported(int D, int kind);
@@ -149,6 +151,12 @@ cudaError_t launch_validate(const int32_t* rows, const int32_t* kv_len, int S, i
 
 // ---------------------------------------------------------------------------
 // small device helpers shared by the kernels of this library
+
+// Which row list (and kv_len entry) slice s reads for KV head g.
+template <class P>
+__device__ __forceinline__ size_t list_of(const P& p, int s, int g) {
+  return p.head_lists ? (size_t)s * p.Hkv + g : (size_t)s;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

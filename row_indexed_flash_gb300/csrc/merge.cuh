@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(64) merge_splits_kernel(const DecodeParams p) 
   const int unit = blockIdx.y;
   const int s = unit / p.Hkv, g = unit % p.Hkv;
   int n_s = p.L;
-  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + s), 0), p.L);
+  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + list_of(p, s, g)), 0), p.L);
   const int ns = n_s > 0 && p.chunk > 0 ? (n_s + p.chunk - 1) / p.chunk : 1;
   const int QV = p.QV;
   const int t = blockIdx.x * blockDim.x + threadIdx.x;

@@ -165,13 +165,13 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
   const int G = p.G, PT = kp.PT;
   const bool causal = p.mask_kind == FA_MASK_CAUSAL;
   int n_s = p.L;
-  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + s), 0), p.L);
+  if (p.kv_len) n_s = min(max(__ldg(p.kv_len + list_of(p, s, g)), 0), p.L);
   const int i0 = qb * 2 * PT;
   const int i_last = min(i0 + 2 * PT, p.Nq) - 1;
   const int lim_max = causal ? n_s - p.Nq + i_last : n_s - 1;
   const int n_vis = max(0, min(n_s, lim_max + 1));
   const int T = (n_vis + BN - 1) / BN;
-  const int32_t* rows_g = p.kv_rows + (size_t)s * p.L;
+  const int32_t* rows_g = p.kv_rows + list_of(p, s, g) * p.L;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -717,25 +717,28 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
   if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
 }
 
-// Before a bf16 launch, per 128-entry KV tile of every slice (one warp each):
+// Before a bf16 launch, per 128-entry KV tile of every list (one warp each):
 // is any listed V value finite and of magnitude 65536 or more (not an f16
 // value: word 1 of the status block gets 1), and is the tile not one
 // contiguous pool run (word 2 counts those, word 3 all tiles)?  The words
-// were zeroed before.
+// were zeroed before.  nl lists of which heads per slice (1: a list is read by
+// every KV head, so whole rows of row_chunks 16-byte chunks are examined; else
+// list l is read by head l % heads alone, and its row_chunks / heads chunks are).
 __global__ void __launch_bounds__(256) prefill_v_scan_kernel(const uint4* v, const int32_t* kv_rows,
-                                                             const int32_t* kv_len, int S, int L, long long R,
-                                                             int row_chunks, int tma_kv, unsigned int* words) {
+                                                             const int32_t* kv_len, int nl, int L, long long R,
+                                                             int row_chunks, int heads, int tma_kv, unsigned int* words) {
   const int lane = threadIdx.x & 31;
   const int tiles_per = (L + pf::BN - 1) / pf::BN;
   const long long nw = (long long)gridDim.x * (blockDim.x >> 5);
   uint32_t bad = 0;
   unsigned gathered = 0, tiles = 0;
-  for (long long e = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); e < (long long)S * tiles_per;
+  for (long long e = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); e < (long long)nl * tiles_per;
        e += nw) {
     const int s = (int)(e / tiles_per), j0 = (int)(e % tiles_per) * pf::BN;
     const int n_s = kv_len ? min(max(__ldg(kv_len + s), 0), L) : L;
     if (j0 >= n_s) continue;
     const int32_t* rows = kv_rows + (size_t)s * L + j0;
+    const int c_lo = (s % heads) * (row_chunks / heads), c_hi = c_lo + row_chunks / heads;
     int r[4];
     #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -758,14 +761,14 @@ __global__ void __launch_bounds__(256) prefill_v_scan_kernel(const uint4* v, con
         int row[4];
         #pragma unroll
         for (int u = 0; u < 4; ++u) row[u] = __shfl_sync(0xffffffffu, r[t], rr + u);
-        for (int i0 = 0; i0 < row_chunks; i0 += 64) {
+        for (int i0 = c_lo; i0 < c_hi; i0 += 64) {
           uint4 w[4][2];
           #pragma unroll
           for (int u = 0; u < 4; ++u) {
             #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int i = i0 + lane + 32 * c;
-              w[u][c] = (row[u] >= 0 && i < row_chunks) ? __ldg(v + (size_t)row[u] * row_chunks + i)
+              w[u][c] = (row[u] >= 0 && i < c_hi) ? __ldg(v + (size_t)row[u] * row_chunks + i)
                                                         : make_uint4(0u, 0u, 0u, 0u);
             }
           }
@@ -834,11 +837,12 @@ cudaError_t prefill_launch(const PrefillParams& a, cudaStream_t st) {
     // words 1-3 of the status block: the scan's V-range flag, gathered and all KV tiles
     cudaError_t e = cudaMemsetAsync(a.err + 1, 0, 3 * sizeof(unsigned int), st);
     if (e != cudaSuccess) return e;
-    const long long tiles = (long long)a.S * ((a.L + pf::BN - 1) / pf::BN);   // one warp each, 8 per block
+    const long long nl = a.head_lists ? (long long)a.S * a.Hkv : a.S;
+    const long long tiles = nl * ((a.L + pf::BN - 1) / pf::BN);   // one warp each, 8 per block
     const long long blocks = (tiles + 7) / 8;
     if (blocks > 0) {
       prefill_v_scan_kernel<<<(unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(
-          static_cast<const uint4*>(a.v), a.kv_rows, a.kv_len, a.S, a.L, a.R, a.Hkv * pf::HD / 8, kp.tma_kv,
+          static_cast<const uint4*>(a.v), a.kv_rows, a.kv_len, (int)nl, a.L, a.R, a.Hkv * pf::HD / 8, a.head_lists ? a.Hkv : 1, kp.tma_kv,
           a.err + 1);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
