@@ -1,6 +1,9 @@
 // Operators on 64-row blocks (pages) of keys: their elementwise bounds, the
 // bound of a query's logits over a block, and the row lists of chosen blocks.
+#include <string.h>
+
 #include "blocks.cuh"
+#include "keyscan.cuh"
 #include "kvread.cuh"
 #include "select.cuh"
 
@@ -99,72 +102,6 @@ cudaError_t bounds_kind(const BoundsParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   bounds_kernel<KIND><<<grid, kBndThreads, smem, st>>>(p, cx);
   return cudaGetLastError();
-}
-
-// ---------------------------------------------------------------------------
-// Scores: score[s, g, b] = max over the slice's queries and g's heads of
-//   sum_d max(q_d, 0) kmax[d] + min(q_d, 0) kmin[d],
-// which no key of the block can exceed as a dot product with that query.
-// One thread per block, eight query vectors at a time; -inf where the
-// sequence has no such block.
-
-constexpr int kScBlocks = 64, kScVec = 8, kScD = 64;
-
-__global__ void __launch_bounds__(kScBlocks) scores_generic_kernel(const ScoresParams p) {
-  __shared__ float lo[kScBlocks][kScD + 1], hi[kScBlocks][kScD + 1];
-  __shared__ float qs[kScVec][kScD];
-  __shared__ int page_s[kScBlocks];
-  const float NEG_INF = __int_as_float(0xff800000);
-  const int tid = threadIdx.x;
-  const int s = blockIdx.z, g = blockIdx.y, b = blockIdx.x * kScBlocks + tid;
-  const int seq = p.slice_seq ? __ldg(p.slice_seq + s) : s;
-  const bool seq_ok = seq >= 0 && seq < p.n_seq;
-  const int n = seq_ok ? max(__ldg(p.seq_len + s), 0) : 0;
-  const int held = min((n + kPage - 1) / kPage, p.max_pages);
-  int page = b < held ? __ldg(p.page_table + (size_t)seq * p.max_pages + b) : -1;
-  if ((long long)page >= p.n_pool_pages) page = -1;
-  page_s[tid] = page;
-  __syncthreads();
-  auto val = [&](const void* t, size_t i) {
-    const uint16_t u = __ldg(static_cast<const uint16_t*>(t) + i);
-    return p.q_bf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-  };
-  float best = NEG_INF;
-  const int nv = p.Nq * p.G;
-  for (int v0 = 0; v0 < nv; v0 += kScVec) {
-    const int m = min(kScVec, nv - v0);
-    float dot[kScVec];
-#pragma unroll
-    for (int t = 0; t < kScVec; ++t) dot[t] = 0.f;
-    for (int d0 = 0; d0 < p.D; d0 += kScD) {
-      const int dn = min(kScD, p.D - d0);
-      __syncthreads();
-      for (int f = tid; f < kScBlocks * dn; f += kScBlocks) {
-        const int e = f / dn, d = f % dn, pg = page_s[e];
-        const size_t at = ((size_t)max(pg, 0) * p.Hkv + g) * p.D + d0 + d;
-        lo[e][d] = pg >= 0 ? val(p.kmin, at) : 0.f;
-        hi[e][d] = pg >= 0 ? val(p.kmax, at) : 0.f;
-      }
-      for (int f = tid; f < m * dn; f += kScBlocks) {
-        const int v = v0 + f / dn;
-        qs[f / dn][f % dn] =
-            val(p.q, (((size_t)s * p.Nq + v / p.G) * p.Hq + g * p.G + v % p.G) * p.D + d0 + f % dn);
-      }
-      __syncthreads();
-      for (int d = 0; d < dn; ++d) {
-        const float l = lo[tid][d], h = hi[tid][d];
-#pragma unroll
-        for (int t = 0; t < kScVec; ++t) {
-          const float q = qs[t][d];
-          dot[t] = fmaf(fmaxf(q, 0.f), h, fmaf(fminf(q, 0.f), l, dot[t]));
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kScVec; ++t)
-      if (t < m) best = max_nan(best, dot[t]);
-  }
-  if (b < p.max_pages) p.score[((size_t)s * p.Hkv + g) * p.max_pages + b] = page >= 0 ? best : NEG_INF;
 }
 
 // ---------------------------------------------------------------------------
@@ -335,9 +272,28 @@ cudaError_t bounds_launch(const BoundsParams& p, cudaStream_t st) {
 }
 
 cudaError_t scores_launch(const ScoresParams& p, cudaStream_t st) {
-  const dim3 grid((p.max_pages + kScBlocks - 1) / kScBlocks, p.Hkv, p.S);
-  scores_generic_kernel<<<grid, kScBlocks, 0, st>>>(p);
-  return cudaGetLastError();
+  KeyScanParams k;
+  memset(&k, 0, sizeof(k));
+  k.q = p.q;
+  k.k[0] = p.kmax;
+  k.k[1] = p.kmin;
+  k.rows = p.page_table;
+  k.len = p.seq_len;
+  k.slice_seq = p.slice_seq;
+  k.out = p.score;
+  k.R = p.n_pool_pages;
+  k.S = p.S;
+  k.Nq = p.Nq;
+  k.Hq = p.Hq;
+  k.Hkv = p.Hkv;
+  k.L = p.max_pages;
+  k.G = p.G;
+  k.NV = p.Nq * p.G;
+  k.n_seq = p.n_seq;
+  k.q_bf16 = p.q_bf16;
+  k.err = p.err;
+  k.wait_ns = p.wait_ns;
+  return keyscan_scores(k, p.D, st);
 }
 
 cudaError_t block_rows_launch(const BlockRowsParams& p, cudaStream_t st) {

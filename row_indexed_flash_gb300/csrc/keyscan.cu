@@ -1,0 +1,1073 @@
+// Few query vectors against many keys on the 5th-generation tensor cores.
+//
+//   weights  acc[s, g, j] = decay * acc + sum_v exp2(c * <q_v, K[row_j, g]> - lse2_v)
+//   scores   score[s, g, b] = max_v <max(q_v, 0), kmax[page_b, g]> + <min(q_v, 0), kmin[page_b, g]>
+//
+// Bound by the bytes of the keys: each is read once.  The keys of a tile are
+// the 128 rows of the MMA's M dimension and the at most 64 query vectors of
+// the KV head its N columns, so a key's products lie in one tensor-memory lane
+// and one thread reduces them in registers, in a fixed order, with nothing
+// exchanged between threads and one fp32 written per key.
+//
+// One CTA per SM walks an even share of all (slice, KV head, tile) triples,
+// whatever the slices' lengths: every CTA adds up the tile counts itself and
+// finds its first triple (list lengths are on the device).  Warps:
+//   0-3    reduction: thread t owns key t of the tile; tensor-memory loads of
+//          its row, the reduction, the update of the output
+//   4      MMA issue (one lane); allocates tensor memory
+//   5      queries of the next (slice, KV head), into one of two buffers: its
+//          rows and, for weights, lse in log2 units and the causal limits
+//   6-13   keys: four warps for each 64-row half of a tile; cp.async of the
+//          listed rows into the 128-byte-swizzled layout, or one TMA tile load
+//          per 64 columns where the half is one contiguous pool run.  The
+//          copies arrive on the stage's barrier by themselves.
+// Scores take two stages per tile (kmax with max(q, 0), then kmin with
+// min(q, 0)), accumulated by the tensor core.  Codes of quantised pools are
+// copied to a ring in shared memory, widened exactly to Q's type by the lanes
+// that copied them, and the row's scale multiplies the product afterwards.
+// Every wait is bounded in time and reported through the workspace's status word.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "keyscan.cuh"
+#include "kvread.cuh"
+#include "tc.cuh"
+#include "tmap.cuh"
+#include "widen.cuh"
+
+namespace far {
+
+namespace ks {
+constexpr int BM = 128;                    // keys per tile
+constexpr int NEPI = 4, W_MMA = 4, W_Q = 5, W_KEY = 6, NKEY = 8;
+constexpr int NWARP = W_KEY + NKEY;
+constexpr int THREADS = NWARP * 32;
+constexpr int MAXST = 8;
+constexpr int MAXN = kScanStreamVec;
+constexpr int SMEM_MAX = 225 * 1024;
+}  // namespace ks
+
+namespace {
+
+enum { SCAN_WEIGHTS = 0, SCAN_SCORES = 1 };
+
+// Shared memory of one instance: sizes that depend on N and the stage counts
+// are computed the same way on both sides.
+struct KsLayout {
+  int N, qb_bytes, nst, tile, ncs, code, off_q, off_k, off_c, off_bar, off_misc, off_l, total;
+};
+
+template <int D, int MODE, int KIND>
+__host__ __device__ inline KsLayout ks_layout(int nv) {
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  KsLayout l;
+  l.N = (nv + 15) / 16 * 16;
+  const int kd = MODE == SCAN_SCORES ? 2 * D : D;
+  l.qb_bytes = l.N * kd * 2;
+  l.tile = ks::BM * D * 2;
+  l.code = QUANT ? ks::BM * kv_row_bytes<KIND>(D) : 0;
+  l.off_q = 0;
+  l.off_k = (2 * l.qb_bytes + 1023) / 1024 * 1024;
+  const int room = ks::SMEM_MAX - 1024 - l.off_k - 2048;
+  if (QUANT) {
+    // operand stages first (two; three for narrow heads), codes with what is left
+    l.nst = D <= 128 ? 2 : 1;
+    l.ncs = (room - l.nst * l.tile) / l.code;
+    l.ncs = l.ncs > ks::MAXST ? ks::MAXST : l.ncs;
+  } else {
+    l.nst = room / l.tile;
+    l.nst = l.nst > ks::MAXST ? ks::MAXST : l.nst;
+    l.ncs = 0;
+  }
+  l.off_c = l.off_k + l.nst * l.tile;
+  l.off_bar = l.off_c + l.ncs * l.code;
+  l.off_misc = l.off_bar + (2 * ks::MAXST + 4 + 4 + 1) * 8;
+  l.off_l = (l.off_misc + 32 + 15) / 16 * 16;
+  l.total = l.off_l + 2 * ks::MAXN * 8 + 1024;
+  return l;
+}
+
+// One CTA's walk over its share of the tiles.
+struct Walk {
+  int s, g, t, T, n;
+};
+
+template <int MODE>
+__device__ __forceinline__ int ks_entries(const KeyScanParams& p, int s) {
+  if (MODE == SCAN_WEIGHTS) return p.len ? min(max(__ldg(p.len + s), 0), p.L) : p.L;
+  if (p.slice_seq) {
+    const int t = __ldg(p.slice_seq + s);
+    if (t < 0 || t >= p.n_seq) return 0;
+  }
+  const int n = max(__ldg(p.len + s), 0);
+  return min(n / kPage + (n % kPage != 0), p.L);
+}
+// Tiles of one (slice, KV head); a slice without blocks still has its scores written.
+template <int MODE>
+__device__ __forceinline__ int ks_tiles(int n) {
+  const int t = n / ks::BM + (n % ks::BM != 0);
+  return MODE == SCAN_SCORES && t == 0 ? 1 : t;
+}
+template <int MODE>
+__device__ __forceinline__ void ks_enter(const KeyScanParams& p, Walk& w) {
+  w.n = ks_entries<MODE>(p, w.s);
+  w.T = ks_tiles<MODE>(w.n);
+}
+template <int MODE>
+__device__ __forceinline__ void ks_next(const KeyScanParams& p, Walk& w) {
+  if (++w.t < w.T) return;
+  w.t = 0;
+  if (++w.g < p.Hkv) return;
+  w.g = 0;
+  do {
+    ++w.s;
+    if (w.s >= p.S) return;   // past the last triple: the caller has none left
+    ks_enter<MODE>(p, w);
+  } while (w.T == 0);
+}
+
+__device__ __forceinline__ float max_nan2(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+__device__ __forceinline__ void ks_wait_drain(uint64_t* b, uint32_t parity) {
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait(b, parity)) {
+    if (globaltimer() - t0 > kWaitLimitNs) return;
+  }
+}
+
+// The MMA lane's wait: polls, so that the time limit holds to the poll.
+__device__ __forceinline__ bool ks_poll(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
+  if (mbar_test_wait(b, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_test_wait(b, parity)) {
+    if (*abort) return false;
+    if (globaltimer() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// 16 bytes of pool codes -> 16-bit values of Q's type, as 16-byte words.
+template <int KIND>
+__device__ __forceinline__ void widen_chunk(const uint4& w, bool bf16, uint4 (&o)[KvChunk<KIND>::N / 8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if constexpr (KIND == KV_I4) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = widen_i4x8(u[t], bf16);
+  } else {
+    uint2 x[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (KIND == KV_F8) {
+        x[t] = widen_e4m3x4(u[t]);
+        if (bf16) {   // every E4M3 value is a bf16 value
+          const float2 a = f16x2_to_f2(x[t].x), b = f16x2_to_f2(x[t].y);
+          x[t] = make_uint2(pack2h(a.x, a.y, true), pack2h(b.x, b.y, true));
+        }
+      } else {
+        x[t] = widen_i8x4(u[t], bf16);
+      }
+    }
+    o[0] = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
+    o[1] = make_uint4(x[2].x, x[2].y, x[3].x, x[3].y);
+  }
+}
+
+// max(q, 0) or min(q, 0) of eight 16-bit values; a NaN stays one.
+__device__ __forceinline__ uint4 sign_part(const uint4& x, bool plus, bool bf16) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (bf16) {
+      const __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f), h = *reinterpret_cast<const __nv_bfloat162*>(&u[t]);
+      const __nv_bfloat162 y = plus ? __hmax2_nan(h, z) : __hmin2_nan(h, z);
+      o[t] = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+      const __half2 z = __floats2half2_rn(0.f, 0.f), h = *reinterpret_cast<const __half2*>(&u[t]);
+      const __half2 y = plus ? __hmax2_nan(h, z) : __hmin2_nan(h, z);
+      o[t] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int D, int MODE, int KIND>
+__global__ void __launch_bounds__(ks::THREADS, 1)
+    keyscan_stream_kernel(const KeyScanParams p, int tma_ok, const __grid_constant__ CUtensorMap t0,
+                          const __grid_constant__ CUtensorMap t1) {
+  using namespace ks;
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;   // stages per tile
+  constexpr int ATOM = BM * 128;                    // one 64-column atom of a key tile
+  constexpr int KT = D / 64;
+  const float INF = __int_as_float(0x7f800000);
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const KsLayout ly = ks_layout<D, MODE, KIND>(p.NV);
+  const int N = ly.N, NST = ly.nst;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + ly.off_bar);
+  uint64_t* k_empty = k_full + MAXST;
+  uint64_t* s_full = k_empty + MAXST;
+  uint64_t* s_empty = s_full + 2;
+  uint64_t* q_full = s_empty + 2;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* drain = q_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + ly.off_misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + ly.off_misc + 4);
+  float* l2 = reinterpret_cast<float*>(sm + ly.off_l);            // [2][MAXN] lse in log2 units
+  int* lim = reinterpret_cast<int*>(sm + ly.off_l) + 2 * MAXN;    // [2][MAXN] n_s-relative causal limits
+  __shared__ long long scan_s[NWARP];
+  __shared__ int walk_s[3];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool bf16 = p.q_bf16 != 0;
+  const unsigned long long wait_ns = p.wait_ns;
+
+  // ---- this CTA's share of the triples
+  long long total = 0;
+  Walk w0;
+  long long mine = 0;
+  {
+    // tiles of all slices, THREADS slices at a time; then the slice that holds
+    // this CTA's first tile
+    for (int pass = 0; pass < 2; ++pass) {
+      long long carry = 0;
+      long long start = 0;
+      if (pass == 1) {
+        start = total * blockIdx.x / gridDim.x;
+        mine = total * (blockIdx.x + 1) / gridDim.x - start;
+        if (mine <= 0) return;
+      }
+      for (int base = 0; base < p.S; base += THREADS) {
+        const int s = base + tid;
+        const int n = s < p.S ? ks_entries<MODE>(p, s) : 0;
+        const int T = s < p.S ? ks_tiles<MODE>(n) : 0;
+        const long long c = (long long)T * p.Hkv;
+        long long x = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) scan_s[warp] = x;
+        __syncthreads();
+        long long before = carry, sum = 0;
+        for (int k = 0; k < NWARP; ++k) {
+          before += k < warp ? scan_s[k] : 0;
+          sum += scan_s[k];
+        }
+        before += x - c;
+        if (pass == 1 && start >= before && start < before + c) {
+          const long long r = start - before;
+          walk_s[0] = s;
+          walk_s[1] = (int)(r / T);
+          walk_s[2] = (int)(r % T);
+        }
+        carry += sum;
+        __syncthreads();
+      }
+      total = carry;
+    }
+    w0.s = walk_s[0];
+    w0.g = walk_s[1];
+    w0.t = walk_s[2];
+    ks_enter<MODE>(p, w0);
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(k_full + i, QUANT ? NKEY : NKEY * 32);
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, NEPI);
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1 + NEPI);   // the MMAs of its last tile, and the reduction warps
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  uint32_t ncols = 32;
+  while ((int)ncols < 2 * N) ncols <<= 1;
+  if (warp == W_MMA) {
+    tmem_alloc(tmem_holder, ncols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+
+  if (warp < NEPI) {
+    // ------------------------------------------------------------ reduction
+    const uint32_t lanes = (uint32_t)warp << 21;   // tensor-memory lane base of this warp: 32 * warp, in bits 16 up
+    Walk w = w0;
+    int unit = 0;
+    // list entry (page) of the thread's key in the next tile, one tile ahead
+    auto entry = [&](const Walk& x) {
+      const int j = x.t * BM + tid;
+      if (j >= x.n) return -1;
+      const int list = MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + x.s) : x.s;
+      const int r = __ldg(p.rows + (size_t)list * p.L + j);
+      return (long long)r < p.R ? r : -1;
+    };
+    int row = entry(w);
+    float scale = 1.f;
+    if (QUANT) scale = row >= 0 ? kv_scale_of(p.k_scale, row, w.g, p.Hkv) : 0.f;
+    bool ok = true;
+    for (long long k = 0; ok && k < mine; ++k) {
+      const int b = (int)(k & 1), qb = unit & 1;
+      const bool first = k == 0 || w.t == 0;
+      const bool last = k + 1 == mine || w.t + 1 == w.T;
+      const int j = w.t * BM + tid;
+      float* out = p.out + ((size_t)w.s * p.Hkv + w.g) * p.L;
+      float old = 0.f;
+      if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < w.n) old = __ldg(out + j);
+      Walk nx = w;
+      int row_nx = -1;
+      float scale_nx = 1.f;
+      if (k + 1 < mine) {
+        ks_next<MODE>(p, nx);
+        row_nx = entry(nx);
+      }
+      if (first && !(ok = __all_sync(0xffffffffu, mbar_wait(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (k >> 1) & 1, abort_flag, wait_ns)))) break;
+      tc_fence_after();
+      if (QUANT) scale_nx = row_nx >= 0 ? kv_scale_of(p.k_scale, row_nx, nx.g, p.Hkv) : 0.f;
+      const float* l2b = l2 + qb * MAXN;
+      const int* limb = lim + qb * MAXN;
+      // causal: every query sees positions up to n - Nq
+      const bool masked = MODE == SCAN_WEIGHTS && p.causal && w.t * BM + BM - 1 > w.n - p.Nq;
+      const float cs = p.c * scale;
+      float r = MODE == SCAN_SCORES ? -INF : 0.f;
+      for (int c0 = 0; c0 < N; c0 += 16) {
+        uint32_t x[16];
+        tmem_ld16(tbase + lanes + b * N + c0, x);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          if (c0 + t >= p.NV) break;
+          const float v = __uint_as_float(x[t]);
+          if (MODE == SCAN_SCORES) {
+            r = max_nan2(r, v);
+          } else {
+            const float l = l2b[c0 + t];
+            const float e = fast_ex2(fmaf(v, cs, -l));
+            const bool see = l < INF || l != l;
+            r += see && (!masked || j <= limb[c0 + t]) ? e : 0.f;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(s_empty + b);
+        if (last) mbar_arrive(q_empty + qb);
+      }
+      if (MODE == SCAN_SCORES) {
+        if (j < w.n) out[j] = row >= 0 ? r : -INF;
+        // past the sequence's blocks: the (slice, KV head)'s last tile fills the rest
+        if (w.t + 1 == w.T)
+          for (int f = w.n + tid; f < p.L; f += NEPI * 32) out[f] = -INF;
+      } else if (j < w.n) {
+        const float add = row >= 0 ? r : 0.f;
+        out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
+      }
+      if (last) ++unit;
+      w = nx;
+      row = row_nx;
+      scale = scale_nx;
+    }
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t id = make_idesc_f16(BM, N, bf16, false);
+      const uint64_t dK = sdesc_sw128(smem_u32(sm + ly.off_k), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + ly.off_q), 16, 1024);
+      const uint32_t qatom = (uint32_t)N * 128;
+      Walk w = w0;
+      int unit = 0;
+      bool ok = true;
+      long long kk = 0;   // stage uses
+      for (long long k = 0; ok && k < mine; ++k) {
+        const int b = (int)(k & 1), qb = unit & 1;
+        const bool first = k == 0 || w.t == 0, last = k + 1 == mine || w.t + 1 == w.T;
+        if (first) ok = ks_poll(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns);
+        ok = ok && ks_poll(s_empty + b, ((k >> 1) & 1) ^ 1, abort_flag, wait_ns);
+#pragma unroll
+        for (int m = 0; m < NK; ++m, ++kk) {
+          const int st = (int)(kk % NST);
+          ok = ok && ks_poll(k_full + st, (kk / NST) & 1, abort_flag, wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          fence_proxy_async_smem();   // the stage's cp.async copies arrived by themselves
+          const uint64_t a = sdesc_at(dK, st * ly.tile), q = sdesc_at(dQ, qb * ly.qb_bytes + m * KT * qatom);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            mma_ss(tbase + b * N, sdesc_at(a, (i >> 2) * ATOM + (i & 3) * 32), sdesc_at(q, (i >> 2) * qatom + (i & 3) * 32),
+                   id, m > 0 || i > 0);
+          tc_commit(k_empty + st);
+        }
+        if (!ok) break;
+        tc_commit(s_full + b);
+        if (last) {
+          tc_commit(q_empty + qb);
+          ++unit;
+        }
+        if (k + 1 < mine) ks_next<MODE>(p, w);
+      }
+      tc_commit(drain);
+      ks_wait_drain(drain, 0);
+    }
+  } else if (warp == W_Q) {
+    // ------------------------------------------------------------ queries
+    Walk w = w0;
+    long long left = mine;
+    constexpr int CPR = D / 8;   // 16-byte chunks of a query vector
+    for (int unit = 0; left > 0; ++unit) {
+      const int qb = unit & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty + qb, ((unit >> 1) & 1) ^ 1, abort_flag, wait_ns))) break;
+      unsigned char* dst = sm + ly.off_q + qb * ly.qb_bytes;
+      const uint16_t* qg = static_cast<const uint16_t*>(p.q);
+#pragma unroll 4
+      for (int f = lane; f < N * CPR; f += 32) {
+        const int v = f / CPR, c = f % CPR;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (v < p.NV)
+          x = __ldg(reinterpret_cast<const uint4*>(qg + (((size_t)w.s * p.Nq + v / p.G) * p.Hq + w.g * p.G + v % p.G) * D) + c);
+        unsigned char* at = dst + (size_t)(c >> 3) * N * 128 + v * 128 + (((c & 7) ^ (v & 7)) << 4);
+        if (MODE == SCAN_SCORES) {
+          *reinterpret_cast<uint4*>(at) = sign_part(x, true, bf16);
+          *reinterpret_cast<uint4*>(at + (size_t)KT * N * 128) = sign_part(x, false, bf16);
+        } else {
+          *reinterpret_cast<uint4*>(at) = x;
+        }
+      }
+      if (MODE == SCAN_WEIGHTS) {
+        for (int v = lane; v < p.NV; v += 32) {
+          const float l = __ldg(p.lse + ((size_t)w.s * p.Nq + v / p.G) * p.Hq + w.g * p.G + v % p.G);
+          l2[qb * MAXN + v] = l == -INF ? INF : l * kLog2e;
+          lim[qb * MAXN + v] = w.n - p.Nq + v / p.G;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + qb);
+      // on to the next (slice, KV head) of the share
+      const int here = w.T - w.t;
+      left -= here;
+      if (left > 0) {
+        w.t = w.T - 1;
+        ks_next<MODE>(p, w);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ keys
+    const int kw = warp - W_KEY;
+    const int half = kw >> 2, quarter = kw & 3;   // 64-row half of the tile, 16 rows of it
+    Walk w = w0;
+    auto list_of_slice = [&](const Walk& x) {
+      return MODE == SCAN_SCORES && p.slice_seq ? (size_t)max(__ldg(p.slice_seq + x.s), 0) : (size_t)x.s;
+    };
+    auto entry = [&](const Walk& x, int e) {   // row (page) of key e of the tile, -1: none
+      const int j = x.t * BM + e;
+      if (j >= x.n) return -1;
+      const int r = __ldg(p.rows + list_of_slice(x) * p.L + j);
+      return r >= 0 && (long long)r < p.R ? r : -1;
+    };
+    if constexpr (!QUANT) {
+      constexpr int CPR = D / 8;
+      unsigned tma_pend = 0, tma_par = 0;
+      int nx0 = entry(w, half * 64 + lane), nx1 = entry(w, half * 64 + 32 + lane);
+      long long kk = 0;
+      bool ok = true;
+      for (long long k = 0; ok && k < mine; ++k) {
+        const int r0 = nx0, r1 = nx1, g = w.g;
+        if (k + 1 < mine) {
+          ks_next<MODE>(p, w);
+          nx0 = entry(w, half * 64 + lane);
+          nx1 = entry(w, half * 64 + 32 + lane);
+        }
+        const int base = __shfl_sync(0xffffffffu, r0, 0);
+        const bool run = __all_sync(0xffffffffu, r0 >= 0 && r0 == base + lane && r1 == base + 32 + lane) && tma_ok;
+#pragma unroll
+        for (int m = 0; m < NK; ++m, ++kk) {
+          const int st = (int)(kk % NST), u = (int)(kk / NST);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, (u & 1) ^ 1, abort_flag, wait_ns)))) break;
+          unsigned char* dst = sm + ly.off_k + st * ly.tile + half * 64 * 128;
+          if (run) {
+            if (quarter == 0 && lane == 0) {
+              mbar_arrive_expect_tx(k_full + st, 64 * D * 2);
+#pragma unroll
+              for (int a = 0; a < KT; ++a) tma_load_3d(dst + a * ATOM, m ? &t1 : &t0, a * 64, g, base, k_full + st);
+              tma_pend |= 1u << st;
+              tma_par = (tma_par & ~(1u << st)) | ((unsigned)(u & 1) << st);
+            } else {
+              mbar_arrive(k_full + st);
+            }
+          } else {
+            const char* src = static_cast<const char*>(p.k[m]);
+#pragma unroll
+            for (int it = 0; it < 16 * CPR / 32; ++it) {
+              const int f = it * 32 + lane;
+              const int e = quarter * 16 + f / CPR, c = f % CPR;   // row of the half, chunk
+              const int ra = __shfl_sync(0xffffffffu, r0, e & 31), rb = __shfl_sync(0xffffffffu, r1, e & 31);
+              const int r = e < 32 ? ra : rb;
+              const bool okr = r >= 0;
+              const size_t go = ((size_t)(okr ? r : 0) * p.Hkv + g) * (D * 2) + c * 16;
+              cp_async16(dst + (c >> 3) * ATOM + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + go, okr);
+            }
+            cp_async_mbar_arrive_noinc(k_full + st);
+          }
+        }
+      }
+      cp_async_wait_all();
+      if (*abort_flag && quarter == 0 && lane == 0) {   // no TMA load may still be writing when the CTA exits
+        for (int i = 0; i < NST; ++i)
+          if ((tma_pend >> i) & 1u) ks_wait_drain(k_full + i, (tma_par >> i) & 1u);
+      }
+    } else {
+      // 16 rows of every tile per warp; each lane copies, and later widens, its
+      // own 16-byte chunks, which lie lane by lane in the code ring
+      constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, NIT = 16 * CPR / 32;
+      static_assert(16 * CPR % 32 == 0, "a warp's chunks fill its lanes");
+      const int NCS = ly.ncs;
+      unsigned char* ring = sm + ly.off_c + kw * 16 * CB;
+      Walk wi = w;                                  // the copies' walk, NCS tiles ahead
+      int nx = entry(wi, kw * 16 + (lane & 15));    // rows of the next tile to copy, lanes 0-15
+      long long ki = 0;
+      auto issue = [&]() {
+        const int row = nx, g = wi.g;
+        if (ki + 1 < mine) {
+          ks_next<MODE>(p, wi);
+          nx = entry(wi, kw * 16 + (lane & 15));
+        }
+        unsigned char* dst = ring + (ki % NCS) * ly.code;
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+          const int f = it * 32 + lane, e = f / CPR, c = f % CPR;
+          const int r = __shfl_sync(0xffffffffu, row, e);
+          const bool okr = r >= 0;
+          cp_async16(dst + f * 16, static_cast<const char*>(p.k[0]) + ((size_t)(okr ? r : 0) * p.Hkv + g) * CB + c * 16, okr);
+        }
+        ++ki;
+      };
+      for (int i = 0; i < NCS - 1; ++i) {
+        if (ki < mine) issue();
+        cp_async_commit();
+      }
+      bool ok = true;
+      for (long long k = 0; ok && k < mine; ++k) {
+        // copies of tile k have landed once at most NCS - 2 later groups are pending
+        switch (NCS) {
+          case 8: cp_async_wait<6>(); break;
+          case 7: cp_async_wait<5>(); break;
+          case 6: cp_async_wait<4>(); break;
+          case 5: cp_async_wait<3>(); break;
+          case 4: cp_async_wait<2>(); break;
+          case 3: cp_async_wait<1>(); break;
+          default: cp_async_wait<0>(); break;
+        }
+        uint4 cw[NIT];
+        const unsigned char* src = ring + (k % NCS) * ly.code;
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) cw[it] = *reinterpret_cast<const uint4*>(src + (it * 32 + lane) * 16);
+        // the ring's next slot is the one tile k - 1 left
+        if (ki < mine) issue();
+        cp_async_commit();
+        const int st = (int)(k % NST), u = (int)(k / NST);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, (u & 1) ^ 1, abort_flag, wait_ns)))) break;
+        unsigned char* dst = sm + ly.off_k + st * ly.tile;
+        constexpr int W = KvChunk<KIND>::N / 8;     // 16-byte words a chunk widens to
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+          const int f = it * 32 + lane, e = kw * 16 + f / CPR, c = (f % CPR) * W;
+          uint4 o[W];
+          widen_chunk<KIND>(cw[it], bf16, o);
+#pragma unroll
+          for (int x = 0; x < W; ++x)
+            *reinterpret_cast<uint4*>(dst + ((c + x) >> 3) * ATOM + e * 128 + ((((c + x) & 7) ^ (e & 7)) << 4)) = o[x];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + st);
+      }
+      cp_async_wait_all();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, ncols);
+  }
+  if (tid == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+}
+
+// ---------------------------------------------------------------------------
+// Many query vectors (prompts): a CTA keeps its keys in shared memory and the
+// queries stream past them.
+//
+// For weights the exponential bounds it (16 a clock and SM, where the tensor
+// core forms 64 products of D = 128 in that time), for scores the tensor core.  A CTA owns
+// NT tiles of 128 keys, so each staged query tile is used NT times; one
+// warpgroup reduces each key tile (thread = key, as above), with two
+// accumulators per key tile so that the products of the next query tile are
+// formed meanwhile.  Two CTAs share an SM where they fit (weights, D <= 128):
+// one's key gather and waits lie under the other's exponentials.
+//   warps 0 .. 4 NT - 1   gather (and widen) the keys, then the reduction
+//   then                  MMA issue; queries: TMA boxes of whole queries
+//                         (weights), or loads that split q into max(q, 0) and
+//                         min(q, 0) tiles (scores, two per query tile)
+namespace kp {
+template <int D, int MODE>
+struct Shape {
+  static constexpr int NT = MODE == SCAN_SCORES && D == 256 ? 1 : 2;      // key tiles
+  static constexpr int N = MODE == SCAN_SCORES && D <= 128 ? 128 : 64;    // query vectors per tile
+  static constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;                  // stages per query tile
+  static constexpr int NST = D == 64 ? 4 : 2;
+  static constexpr int CTAS = MODE == SCAN_WEIGHTS && D <= 128 ? 2 : 1;   // per SM
+  static constexpr int ATOM = ks::BM * 128;
+  static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
+  static constexpr int QST = N * D * 2;               // one query stage
+  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = MODE == SCAN_SCORES ? 4 : 1;
+  static constexpr int THREADS = (W_Q + NQW) * 32;
+  static constexpr int OFF_Q = NT * NK * KMAT;
+  static constexpr int OFF_BAR = OFF_Q + NST * QST;
+  static constexpr int NBAR = 1 + 2 * NST + 4 * NT + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NST][N] lse, [NST][N] limits, [NST] flags
+  static constexpr int OFF_IDX = OFF_L + (MODE == SCAN_WEIGHTS ? NST * N * 8 + NST * 4 : 0);
+  static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
+  static constexpr int SMEM = USED + 1024;
+  static constexpr uint32_t COLS = NT * 2 * N;
+  static_assert(COLS * CTAS <= 512 && (COLS & (COLS - 1)) == 0, "tensor memory");
+  static_assert((SMEM + 1024) * CTAS <= 227 * 1024 + 1024, "shared memory");
+};
+}  // namespace kp
+
+template <int D, int MODE, int KIND>
+__global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, MODE>::CTAS))
+    keyscan_prompt_kernel(const KeyScanParams p, int PT, int q_box, const __grid_constant__ CUtensorMap tq) {
+  using Sh = kp::Shape<D, MODE>;
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  constexpr int NT = Sh::NT, N = Sh::N, NK = Sh::NK, NST = Sh::NST, KT = D / 64, KEYS = NT * ks::BM;
+  const float INF = __int_as_float(0x7f800000);
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* key_full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
+  uint64_t* q_full = key_full + 1;
+  uint64_t* q_empty = q_full + NST;
+  uint64_t* s_full = q_empty + NST;      // [NT][2]
+  uint64_t* s_empty = s_full + 2 * NT;   // [NT][2]
+  uint64_t* drain = s_empty + 2 * NT;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + Sh::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::OFF_MISC + 4);
+  float* l2 = reinterpret_cast<float*>(sm + Sh::OFF_L);
+  int* lim = reinterpret_cast<int*>(l2 + NST * N);
+  int* odd = lim + NST * N;              // a column of the stage's tile adds nothing, whatever its product
+  int* idx = reinterpret_cast<int*>(sm + Sh::OFF_IDX);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * KEYS;
+  const bool bf16 = p.q_bf16 != 0;
+  const unsigned long long wait_ns = p.wait_ns;
+  const int n = ks_entries<MODE>(p, s);
+  float* out = p.out + ((size_t)s * p.Hkv + g) * p.L;
+  if (j0 >= n) {   // no such keys; blocks past the sequence score -inf
+    if (MODE == SCAN_SCORES)
+      for (int j = j0 + tid; j < min(j0 + KEYS, p.L); j += Sh::THREADS) out[j] = -INF;
+    return;
+  }
+  // query tiles of PT queries (weights; N vectors for scores); a causal CTA
+  // starts at the first query that sees its first key
+  int t0 = 0;
+  const int nt = MODE == SCAN_SCORES ? (p.NV + N - 1) / N : (p.Nq + PT - 1) / PT;
+  if (MODE == SCAN_WEIGHTS && p.causal) t0 = min(nt, max(0, j0 - (n - p.Nq)) / PT);
+  const int T = nt - t0;
+
+  if (tid == 0) {
+    mbar_init(key_full, Sh::NEPI * 32);
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(q_full + i, MODE == SCAN_SCORES ? Sh::NQW : 1);
+      mbar_init(q_empty + i, MODE == SCAN_SCORES ? 1 : 1 + Sh::NEPI);
+    }
+    for (int i = 0; i < 2 * NT; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_empty + i, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == Sh::W_MMA) {
+    tmem_alloc(tmem_holder, Sh::COLS);
+    tmem_relinquish();
+  }
+  const size_t list = MODE == SCAN_SCORES && p.slice_seq ? (size_t)__ldg(p.slice_seq + s) : (size_t)s;
+  for (int e = tid; e < KEYS; e += Sh::THREADS) {
+    const int r = j0 + e < n ? __ldg(p.rows + list * p.L + j0 + e) : -1;
+    idx[e] = r >= 0 && (long long)r < p.R ? r : -1;
+  }
+  if (MODE == SCAN_WEIGHTS && q_box * p.G < N) {
+    // rows of a query tile that no box writes
+    for (int f = tid; f < NST * Sh::QST / 16; f += Sh::THREADS)
+      reinterpret_cast<uint4*>(sm + Sh::OFF_Q)[f] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_holder;
+
+  if (warp < Sh::NEPI) {
+    // ------------------------------------------------------------ keys
+    if constexpr (QUANT) {
+      constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, W = KvChunk<KIND>::N / 8;
+#pragma unroll 4
+      for (int f = tid; f < KEYS * CPR; f += KEYS) {
+        const int e = f / CPR, c = f % CPR, r = idx[e];
+        uint4 cw = make_uint4(0u, 0u, 0u, 0u), o[W];
+        if (r >= 0)
+          cw = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k[0]) + ((size_t)r * p.Hkv + g) * CB) + c);
+        widen_chunk<KIND>(cw, bf16, o);
+        unsigned char* dst = sm + (e >> 7) * Sh::KMAT + (e & 127) * 128;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+          const int cc = c * W + x;
+          *reinterpret_cast<uint4*>(dst + (cc >> 3) * Sh::ATOM + (((cc & 7) ^ (e & 7)) << 4)) = o[x];
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(key_full);
+    } else {
+      constexpr int CPR = D / 8;
+#pragma unroll
+      for (int m = 0; m < NK; ++m) {
+        const char* src = static_cast<const char*>(p.k[m]);
+#pragma unroll 8
+        for (int f = tid; f < KEYS * CPR; f += KEYS) {
+          const int e = f / CPR, c = f % CPR, r = idx[e];
+          const size_t go = ((size_t)max(r, 0) * p.Hkv + g) * (D * 2) + c * 16;
+          cp_async16(sm + ((e >> 7) * NK + m) * Sh::KMAT + (c >> 3) * Sh::ATOM + (e & 127) * 128 + (((c & 7) ^ (e & 7)) << 4),
+                     src + go, r >= 0);
+        }
+      }
+      cp_async_mbar_arrive_noinc(key_full);
+    }
+    // ------------------------------------------------------------ reduction
+    const int kt = warp >> 2;                              // this warpgroup's key tile
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const int e = kt * ks::BM + (tid & 127), j = j0 + e;
+    const int row = idx[e];
+    const float cs = QUANT && row >= 0 ? p.c * kv_scale_of(p.k_scale, row, g, p.Hkv) : p.c;
+    float old = 0.f;
+    if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldg(out + j);
+    float total = MODE == SCAN_SCORES ? -INF : 0.f;
+    bool ok = true;
+    for (int t = 0; t < T; ++t) {
+      const int b = t & 1, st = t % NST;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + kt * 2 + b, (t >> 1) & 1, abort_flag, wait_ns)))) break;
+      tc_fence_after();
+      const uint32_t at = tbase + lanes + (kt * 2 + b) * N;
+      if constexpr (MODE == SCAN_SCORES) {
+        const int m = p.NV - t * N;      // real columns of the tile
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          uint32_t x[32];
+          tmem_ld32(at + c0, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c0 + i < m) total = max_nan2(total, __uint_as_float(x[i]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
+      } else {
+        const float4* l4 = reinterpret_cast<const float4*>(l2 + st * N);
+        const int4* m4 = reinterpret_cast<const int4*>(lim + st * N);
+        // this warp's highest key against the tile's first query
+        const bool masked = odd[st] || (p.causal && j0 + kt * ks::BM + (warp & 3) * 32 + 31 > lim[st * N]);
+        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          uint32_t x[32];
+          tmem_ld32(at + c0, x);
+          if (c0 + 32 == N) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
+          }
+          if (!masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 l = l4[c0 / 4 + i];
+              r0 += fast_ex2(fmaf(__uint_as_float(x[4 * i]), cs, -l.x));
+              r1 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 1]), cs, -l.y));
+              r2 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 2]), cs, -l.z));
+              r3 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 3]), cs, -l.w));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 l = l4[c0 / 4 + i];
+              const int4 m = m4[c0 / 4 + i];
+              const float lv[4] = {l.x, l.y, l.z, l.w};
+              const int mv[4] = {m.x, m.y, m.z, m.w};
+              float ev[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float ex = fast_ex2(fmaf(__uint_as_float(x[4 * i + u]), cs, -lv[u]));
+                ev[u] = (lv[u] < INF || lv[u] != lv[u]) && j <= mv[u] ? ex : 0.f;
+              }
+              r0 += ev[0];
+              r1 += ev[1];
+              r2 += ev[2];
+              r3 += ev[3];
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + st);
+        total += (r0 + r1) + (r2 + r3);
+      }
+    }
+    if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
+    if (j < n) {
+      if (MODE == SCAN_SCORES) {
+        out[j] = row >= 0 ? total : -INF;
+      } else {
+        const float add = row >= 0 ? total : 0.f;
+        out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
+      }
+    } else if (MODE == SCAN_SCORES && j < p.L) {
+      out[j] = -INF;
+    }
+  } else if (warp == Sh::W_MMA) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t id = make_idesc_f16(ks::BM, N, bf16, false);
+      const uint64_t dK = sdesc_sw128(smem_u32(sm), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
+      bool ok = ks_poll(key_full, 0, abort_flag, wait_ns);
+      fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
+      int kk = 0;
+      for (int t = 0; ok && t < T; ++t) {
+        const int b = t & 1;
+#pragma unroll
+        for (int m = 0; m < NK; ++m, ++kk) {
+          const int st = kk % NST;
+          ok = ok && ks_poll(q_full + st, (kk / NST) & 1, abort_flag, wait_ns);
+          for (int kt = 0; ok && kt < NT; ++kt) {
+            if (m == 0) ok = ks_poll(s_empty + kt * 2 + b, ((t >> 1) & 1) ^ 1, abort_flag, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT), q = sdesc_at(dQ, st * Sh::QST);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              mma_ss(tbase + (kt * 2 + b) * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
+                     sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
+            if (m == NK - 1) tc_commit(s_full + kt * 2 + b);
+          }
+          if (!ok) break;
+          tc_commit(q_empty + st);
+        }
+      }
+      tc_commit(drain);
+      ks_wait_drain(drain, 0);
+    }
+  } else if (MODE == SCAN_WEIGHTS) {
+    // ------------------------------------------------------------ queries by TMA
+    unsigned pend = 0, par = 0;
+    auto lse_of = [&](int t, int v) {   // log2-unit lse of column v of query tile t; +inf: adds nothing
+      const int i = (t0 + t) * PT + v / p.G;
+      if (t >= T || v >= PT * p.G || i >= p.Nq) return INF;
+      const float l = __ldg(p.lse + ((size_t)s * p.Nq + i) * p.Hq + g * p.G + v % p.G);
+      return l == -INF ? INF : l * kLog2e;
+    };
+    float nl[N / 32];
+#pragma unroll
+    for (int u = 0; u < N / 32; ++u) nl[u] = lse_of(0, lane + 32 * u);
+    for (int t = 0; t < T; ++t) {
+      const int st = t % NST, u2 = t / NST;
+      if (!__all_sync(0xffffffffu, mbar_wait(q_empty + st, (u2 & 1) ^ 1, abort_flag, wait_ns))) break;
+      bool hide = false;
+#pragma unroll
+      for (int u = 0; u < N / 32; ++u) {
+        const int v = lane + 32 * u;
+        l2[st * N + v] = nl[u];
+        lim[st * N + v] = n - p.Nq + (t0 + t) * PT + v / p.G;
+        if (!p.causal) lim[st * N + v] = 0x7fffffff;
+        hide = hide || !(nl[u] < INF);
+        nl[u] = lse_of(t + 1, v);
+      }
+      hide = __any_sync(0xffffffffu, hide);
+      if (lane == 0) {
+        odd[st] = hide;
+        mbar_arrive_expect_tx(q_full + st, (uint32_t)KT * q_box * p.G * 128u);
+#pragma unroll
+        for (int a = 0; a < KT; ++a)
+          tma_load_3d(sm + Sh::OFF_Q + st * Sh::QST + a * N * 128, &tq, a * 64, g * p.G, s * p.Nq + (t0 + t) * PT, q_full + st);
+        pend |= 1u << st;
+        par = (par & ~(1u << st)) | ((unsigned)(u2 & 1) << st);
+      }
+      __syncwarp();
+    }
+    if (*abort_flag && lane == 0) {   // no TMA load may still be writing when the CTA exits
+      for (int i = 0; i < NST; ++i)
+        if ((pend >> i) & 1u) ks_wait_drain(q_full + i, (par >> i) & 1u);
+    }
+  } else {
+    // ------------------------------------------------------------ queries, split by sign
+    constexpr int CPR = D / 8, STEP = Sh::NQW * 32;
+    const int qt = tid - Sh::W_Q * 32;
+    const uint16_t* qg = static_cast<const uint16_t*>(p.q);
+    bool ok = true;
+    int kk = 0;
+    for (int t = 0; ok && t < T; ++t) {
+#pragma unroll
+      for (int m = 0; m < NK; ++m, ++kk) {
+        const int st = kk % NST;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, ((kk / NST) & 1) ^ 1, abort_flag, wait_ns)))) break;
+        unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
+#pragma unroll 8
+        for (int f = qt; f < N * CPR; f += STEP) {
+          const int r = f / CPR, c = f % CPR, v = t * N + r;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (v < p.NV)
+            x = __ldg(reinterpret_cast<const uint4*>(qg + (((size_t)s * p.Nq + v / p.G) * p.Hq + g * p.G + v % p.G) * D) + c);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x, m == 0, bf16);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + st);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Sh::W_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, Sh::COLS);
+  }
+  if (tid == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+int ks_sms() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  if (cached[dev] == 0 && cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cached[dev] = 0;
+  return cached[dev] > 0 ? cached[dev] : 1;
+}
+
+bool ks_map(CUtensorMap* m, const void* base, bool bf16, int D, int Hkv, long long R) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)R};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * Hkv * 2};
+  const cuuint32_t box[3] = {64, 1, 64};
+  return tmap_encode_3d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, dims, strides,
+                        box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, int MODE, int KIND>
+cudaError_t ks_stream(const KeyScanParams& p, cudaStream_t st) {
+  auto kern = keyscan_stream_kernel<D, MODE, KIND>;
+  const KsLayout ly = ks_layout<D, MODE, KIND>(p.NV);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ks::SMEM_MAX);
+  if (e != cudaSuccess) return e;
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  CUtensorMap t0, t1;
+  memset(&t0, 0, sizeof(t0));
+  memset(&t1, 0, sizeof(t1));
+  int tma = 0;
+  if (!QUANT && p.R >= 64) {
+    tma = 1;
+    if (!ks_map(&t0, p.k[0], p.q_bf16 != 0, D, p.Hkv, p.R)) return cudaErrorInvalidValue;
+    if (MODE == SCAN_SCORES && !ks_map(&t1, p.k[1], p.q_bf16 != 0, D, p.Hkv, p.R)) return cudaErrorInvalidValue;
+  }
+  const long long most = (long long)p.S * p.Hkv * ((p.L + ks::BM - 1) / ks::BM);
+  const int sms = ks_sms();
+  const int grid = (int)(most < sms ? most : sms);
+  kern<<<grid, ks::THREADS, ly.total, st>>>(p, tma, t0, t1);
+  return cudaGetLastError();
+}
+
+template <int D, int MODE, int KIND>
+cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
+  using Sh = kp::Shape<D, MODE>;
+  auto kern = keyscan_prompt_kernel<D, MODE, KIND>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tq;
+  memset(&tq, 0, sizeof(tq));
+  int PT = 0, q_box = 0;
+  if (MODE == SCAN_WEIGHTS) {
+    PT = Sh::N / p.G;
+    const long long queries = (long long)p.S * p.Nq;
+    q_box = (int)(queries < PT ? queries : PT);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)queries};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * p.Hq * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)q_box};
+    if (!tmap_encode_3d(&tq, p.q_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.q, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  const int keys = Sh::NT * ks::BM;
+  kern<<<dim3((p.L + keys - 1) / keys, p.Hkv, p.S), Sh::THREADS, Sh::SMEM, st>>>(p, PT, q_box, tq);
+  return cudaGetLastError();
+}
+
+template <int D, int MODE, int KIND>
+cudaError_t ks_launch(const KeyScanParams& p, cudaStream_t st) {
+  return p.NV <= kScanStreamVec ? ks_stream<D, MODE, KIND>(p, st) : ks_prompt<D, MODE, KIND>(p, st);
+}
+
+template <int KIND>
+cudaError_t ks_weights_kind(const KeyScanParams& p, int D, cudaStream_t st) {
+  if (D == 64) return ks_launch<64, SCAN_WEIGHTS, KIND>(p, st);
+  if (D == 128) return ks_launch<128, SCAN_WEIGHTS, KIND>(p, st);
+  return ks_launch<256, SCAN_WEIGHTS, KIND>(p, st);
+}
+
+}  // namespace
+
+// G <= 64: a query tile of the prompt form holds whole queries.
+bool keyscan_supported(int D, int G) { return (D == 64 || D == 128 || D == 256) && G <= 64; }
+
+cudaError_t keyscan_weights(const KeyScanParams& p, int D, int kind, cudaStream_t st) {
+  switch (kind) {
+    // the 16-bit kinds differ only in the instruction descriptor's type
+    case KV_BF16:
+    case KV_F16: return ks_weights_kind<KV_BF16>(p, D, st);
+    case KV_I8: return ks_weights_kind<KV_I8>(p, D, st);
+    case KV_I4: return ks_weights_kind<KV_I4>(p, D, st);
+    case KV_F8: return ks_weights_kind<KV_F8>(p, D, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t keyscan_scores(const KeyScanParams& p, int D, cudaStream_t st) {
+  if (D == 64) return ks_launch<64, SCAN_SCORES, KV_BF16>(p, st);
+  if (D == 128) return ks_launch<128, SCAN_SCORES, KV_BF16>(p, st);
+  if (D == 256) return ks_launch<256, SCAN_SCORES, KV_BF16>(p, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace far

@@ -15,7 +15,10 @@
 // memory, one thread per key forms the logits of eight query vectors at a time
 // (broadcast reads of the staged queries) and adds their weights.  Rows are
 // padded by one word, so the 32 keys of a warp lie on 32 banks.
+#include <string.h>
+
 #include "fa_internal.cuh"
+#include "keyscan.cuh"
 #include "kvread.cuh"
 #include "weights.cuh"
 
@@ -117,6 +120,34 @@ cudaError_t weights_generic(const WeightsParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t weights_launch(const WeightsParams& p, cudaStream_t st) {
+  const int nv = p.Nq * p.G;
+  if (p.mask_kind != FA_MASK_DENSE && reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && keyscan_supported(p.D, p.G)) {
+    KeyScanParams k;
+    memset(&k, 0, sizeof(k));
+    k.q = p.q;
+    k.k[0] = p.k;
+    k.k_scale = p.k_scale;
+    k.rows = p.kv_rows;
+    k.len = p.kv_len;
+    k.lse = p.lse;
+    k.out = p.acc;
+    k.R = p.R;
+    k.S = p.S;
+    k.Nq = p.Nq;
+    k.Hq = p.Hq;
+    k.Hkv = p.Hkv;
+    k.L = p.L;
+    k.G = p.G;
+    k.NV = nv;
+    k.n_seq = p.S;
+    k.q_bf16 = p.q_bf16;
+    k.causal = p.mask_kind == FA_MASK_CAUSAL;
+    k.c = p.scale * kLog2e;
+    k.decay = p.decay;
+    k.err = p.err;
+    k.wait_ns = p.wait_ns;
+    return keyscan_weights(k, p.D, p.kind, st);
+  }
   switch (p.kind) {
     case KV_BF16: return weights_generic<KV_BF16>(p, st);
     case KV_F16: return weights_generic<KV_F16>(p, st);

@@ -210,3 +210,52 @@ def test_weights_read_pool_rows_past_two_gigabytes():
     got = far.fa_rows_weights(q, kd, rows, 1.0 / 128, lse, k_scale=ks, check_status=True)[0]
     want = 2.0 * np.exp([0.0, 2.0, 1.0, 0.0])
     assert np.allclose(got[:, :4].cpu().numpy(), np.tile(want, (8, 1)), rtol=2.0 ** -18) and (got[:, 4:] == 0).all()
+
+
+def paged_rows(seed, S, L, R, run):
+    """Lists of whole runs of `run` consecutive rows in random order, the last one cut."""
+    g = synth.rng(seed)
+    starts = np.stack([g.permutation(R // run)[: -(-L // run)] * run for _ in range(S)])
+    return (starts[:, :, None] + np.arange(run)).reshape(S, -1)[:, :L].astype(np.int32)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "i8", "i4", "f8"])
+@pytest.mark.parametrize("case", [
+    dict(S=3, Nq=1, Hq=8, Hkv=2, D=128, L=5000, run=64, lens=[5000, 63, 4097]),
+    dict(S=2, Nq=2, Hq=16, Hkv=2, D=64, L=9000, run=128, lens=[9000, 8191]),
+    dict(S=2, Nq=4, Hq=8, Hkv=1, D=256, L=3000, run=64, lens=[1, 3000]),
+    dict(S=2, Nq=100, Hq=8, Hkv=2, D=128, L=3000, run=64, lens=[2999, 1500]),
+])
+def test_weights_over_pages(case, kv):
+    c = dict(case)
+    run_rows, lens = c.pop("run"), c.pop("lens")
+    p, kd, ks, k64 = make(300 + c["L"], kv, "f16" if kv == "f16" else "bf16", R=16384, causal=True, pad_frac=0.0, **c)
+    p.kv_rows = paged_rows(301, c["S"], c["L"], 16384, run_rows)
+    p.kv_len = np.asarray(lens, np.int32)
+    p.kv_rows[0, 2] = -1                      # a hole in a page
+    check(p, kd, ks, k64)
+
+
+def test_weights_of_many_short_slices():
+    # more slices than threads of a block, some empty, every share crossing many of them
+    S = 1100
+    p, kd, ks, k64 = make(320, S=S, Nq=1, Hq=2, Hkv=2, D=64, R=1024, L=140)
+    p.kv_len = synth.rng(321).integers(0, 141, size=S).astype(np.int32)
+    p.kv_len[::7] = 0
+    check(p, kd, ks, k64)
+
+
+@pytest.mark.parametrize("kv,Nq", [("bf16", 1), ("i8", 1), ("bf16", 40)])
+def test_weights_report_an_expired_wait_and_recover(kv, Nq):
+    p, kd, ks, k64 = make(330, kv, S=2, Nq=Nq, Hq=8, Hkv=2, D=128, R=8192, L=6000)
+    lse = torch.zeros((2, Nq, 8), dtype=torch.float32, device="cuda")
+    q, rows = dev_bits(p.q, "bf16"), torch.from_numpy(p.kv_rows).cuda()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = far.fa_rows_weights(q, kd, rows, p.scale, lse, k_scale=ks, workspace=ws, check_status=True)
+    far.fa_set_wait_limit_ns(1)
+    try:
+        far.fa_rows_weights(q, kd, rows, p.scale, lse, k_scale=ks, workspace=ws)
+        assert far.fa_rows_status(ws, clear=True) & far.FA_WS_WAIT_EXPIRED
+    finally:
+        far.fa_set_wait_limit_ns(0)
+    assert torch.equal(far.fa_rows_weights(q, kd, rows, p.scale, lse, k_scale=ks, workspace=ws, check_status=True), want)
