@@ -45,6 +45,7 @@ constexpr int NWARP = W_KEY + NKEY;
 constexpr int THREADS = NWARP * 32;
 constexpr int MAXST = 8;
 constexpr int MAXN = kScanStreamVec;
+constexpr int PRE = 4;                     // tiles ahead that list entries are loaded
 constexpr int SMEM_MAX = 225 * 1024;
 }  // namespace ks
 
@@ -321,7 +322,13 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       const int r = __ldg(p.rows + (size_t)list * p.L + j);
       return (long long)r < p.R ? r : -1;
     };
+    auto before = [&](const Walk& x) {   // the entry's accumulator
+      const int j = x.t * BM + tid;
+      if (MODE != SCAN_WEIGHTS || p.decay == 0.f || j >= x.n) return 0.f;
+      return __ldg(p.out + ((size_t)x.s * p.Hkv + x.g) * p.L + j);
+    };
     int row = entry(w);
+    float old = before(w);
     float scale = 1.f;
     if (QUANT) scale = row >= 0 ? kv_scale_of(p.k_scale, row, w.g, p.Hkv) : 0.f;
     bool ok = true;
@@ -331,14 +338,13 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       const bool last = k + 1 == mine || w.t + 1 == w.T;
       const int j = w.t * BM + tid;
       float* out = p.out + ((size_t)w.s * p.Hkv + w.g) * p.L;
-      float old = 0.f;
-      if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < w.n) old = __ldg(out + j);
       Walk nx = w;
       int row_nx = -1;
-      float scale_nx = 1.f;
+      float scale_nx = 1.f, old_nx = 0.f;
       if (k + 1 < mine) {
         ks_next<MODE>(p, nx);
         row_nx = entry(nx);
+        old_nx = before(nx);
       }
       if (first && !(ok = __all_sync(0xffffffffu, mbar_wait(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns)))) break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (k >> 1) & 1, abort_flag, wait_ns)))) break;
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       w = nx;
       row = row_nx;
       scale = scale_nx;
+      old = old_nx;
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issue
@@ -487,16 +494,31 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
     if constexpr (!QUANT) {
       constexpr int CPR = D / 8;
       unsigned tma_pend = 0, tma_par = 0;
-      int nx0 = entry(w, half * 64 + lane), nx1 = entry(w, half * 64 + 32 + lane);
+      // list entries PRE tiles ahead: a tile's share of HBM time is shorter
+      // than the latency of a list load
+      int nx0[PRE], nx1[PRE];
+      Walk wp = w;
+      long long kp = 0;
+      auto fetch = [&](int& a, int& b) {
+        if (kp < mine) {
+          a = entry(wp, half * 64 + lane);
+          b = entry(wp, half * 64 + 32 + lane);
+          if (++kp < mine) ks_next<MODE>(p, wp);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < PRE; ++i) fetch(nx0[i], nx1[i]);
       long long kk = 0;
       bool ok = true;
       for (long long k = 0; ok && k < mine; ++k) {
-        const int r0 = nx0, r1 = nx1, g = w.g;
-        if (k + 1 < mine) {
-          ks_next<MODE>(p, w);
-          nx0 = entry(w, half * 64 + lane);
-          nx1 = entry(w, half * 64 + 32 + lane);
+        const int r0 = nx0[0], r1 = nx1[0], g = w.g;
+#pragma unroll
+        for (int i = 0; i + 1 < PRE; ++i) {
+          nx0[i] = nx0[i + 1];
+          nx1[i] = nx1[i + 1];
         }
+        fetch(nx0[PRE - 1], nx1[PRE - 1]);
+        if (k + 1 < mine) ks_next<MODE>(p, w);
         const int base = __shfl_sync(0xffffffffu, r0, 0);
         const bool run = __all_sync(0xffffffffu, r0 >= 0 && r0 == base + lane && r1 == base + 32 + lane) && tma_ok;
 #pragma unroll
@@ -542,15 +564,23 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       static_assert(16 * CPR % 32 == 0, "a warp's chunks fill its lanes");
       const int NCS = ly.ncs;
       unsigned char* ring = sm + ly.off_c + kw * 16 * CB;
-      Walk wi = w;                                  // the copies' walk, NCS tiles ahead
-      int nx = entry(wi, kw * 16 + (lane & 15));    // rows of the next tile to copy, lanes 0-15
-      long long ki = 0;
-      auto issue = [&]() {
-        const int row = nx, g = wi.g;
-        if (ki + 1 < mine) {
-          ks_next<MODE>(p, wi);
-          nx = entry(wi, kw * 16 + (lane & 15));
+      Walk wi = w, wp = w;                          // the copies' walk, NCS tiles ahead; the list entries', PRE more
+      int nx[PRE];                                  // rows of the next tiles to copy, lanes 0-15
+      long long ki = 0, kp = 0;
+      auto fetch = [&](int& a) {
+        if (kp < mine) {
+          a = entry(wp, kw * 16 + (lane & 15));
+          if (++kp < mine) ks_next<MODE>(p, wp);
         }
+      };
+#pragma unroll
+      for (int i = 0; i < PRE; ++i) fetch(nx[i]);
+      auto issue = [&]() {
+        const int row = nx[0], g = wi.g;
+#pragma unroll
+        for (int i = 0; i + 1 < PRE; ++i) nx[i] = nx[i + 1];
+        fetch(nx[PRE - 1]);
+        if (ki + 1 < mine) ks_next<MODE>(p, wi);
         unsigned char* dst = ring + (ki % NCS) * ly.code;
 #pragma unroll
         for (int it = 0; it < NIT; ++it) {
@@ -633,11 +663,12 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 namespace kp {
 template <int D, int MODE>
 struct Shape {
-  static constexpr int NT = MODE == SCAN_SCORES && D == 256 ? 1 : 2;      // key tiles
-  static constexpr int N = MODE == SCAN_SCORES && D <= 128 ? 128 : 64;    // query vectors per tile
+  static constexpr int NT = MODE == SCAN_SCORES ? 1 : 2;                  // key tiles
+  static constexpr int N = 64;                                            // query vectors per tile
   static constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;                  // stages per query tile
   static constexpr int NST = D == 64 ? 4 : 2;
-  static constexpr int CTAS = MODE == SCAN_WEIGHTS && D <= 128 ? 2 : 1;   // per SM
+  static constexpr int NL = 4;                                            // query tiles whose lse are on chip
+  static constexpr int CTAS = D <= 128 ? 2 : 1;                           // per SM
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
   static constexpr int QST = N * D * 2;               // one query stage
@@ -645,10 +676,10 @@ struct Shape {
   static constexpr int THREADS = (W_Q + NQW) * 32;
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
-  static constexpr int NBAR = 1 + 2 * NST + 4 * NT + 1;
+  static constexpr int NBAR = 1 + 2 * NST + 4 * NT + 1 + 2 * NL;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NST][N] lse, [NST][N] limits, [NST] flags
-  static constexpr int OFF_IDX = OFF_L + (MODE == SCAN_WEIGHTS ? NST * N * 8 + NST * 4 : 0);
+  static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NL][N] lse, [NL][N] limits, [NL] flags
+  static constexpr int OFF_IDX = OFF_L + (MODE == SCAN_WEIGHTS ? NL * N * 8 + NL * 4 : 0);
   static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
   static constexpr int SMEM = USED + 1024;
   static constexpr uint32_t COLS = NT * 2 * N;
@@ -662,7 +693,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     keyscan_prompt_kernel(const KeyScanParams p, int PT, int q_box, const __grid_constant__ CUtensorMap tq) {
   using Sh = kp::Shape<D, MODE>;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
-  constexpr int NT = Sh::NT, N = Sh::N, NK = Sh::NK, NST = Sh::NST, KT = D / 64, KEYS = NT * ks::BM;
+  constexpr int NT = Sh::NT, N = Sh::N, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64, KEYS = NT * ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -672,11 +703,13 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
   uint64_t* s_full = q_empty + NST;      // [NT][2]
   uint64_t* s_empty = s_full + 2 * NT;   // [NT][2]
   uint64_t* drain = s_empty + 2 * NT;
+  uint64_t* l_full = drain + 1;          // [NL] lse, limits and flag of a query tile
+  uint64_t* l_empty = l_full + NL;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + Sh::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::OFF_MISC + 4);
   float* l2 = reinterpret_cast<float*>(sm + Sh::OFF_L);
-  int* lim = reinterpret_cast<int*>(l2 + NST * N);
-  int* odd = lim + NST * N;              // a column of the stage's tile adds nothing, whatever its product
+  int* lim = reinterpret_cast<int*>(l2 + NL * N);
+  int* odd = lim + NL * N;              // a column of the stage's tile adds nothing, whatever its product
   int* idx = reinterpret_cast<int*>(sm + Sh::OFF_IDX);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -701,7 +734,11 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     mbar_init(key_full, Sh::NEPI * 32);
     for (int i = 0; i < NST; ++i) {
       mbar_init(q_full + i, MODE == SCAN_SCORES ? Sh::NQW : 1);
-      mbar_init(q_empty + i, MODE == SCAN_SCORES ? 1 : 1 + Sh::NEPI);
+      mbar_init(q_empty + i, 1);
+    }
+    for (int i = 0; i < NL; ++i) {
+      mbar_init(l_full + i, 1);
+      mbar_init(l_empty + i, Sh::NEPI);
     }
     for (int i = 0; i < 2 * NT; ++i) {
       mbar_init(s_full + i, 1);
@@ -777,34 +814,47 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     float total = MODE == SCAN_SCORES ? -INF : 0.f;
     bool ok = true;
     for (int t = 0; t < T; ++t) {
-      const int b = t & 1, st = t % NST;
+      const int b = t & 1, sl = t % NL;
+      if (MODE == SCAN_WEIGHTS &&
+          !(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (t / NL) & 1, abort_flag, wait_ns))))
+        break;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + kt * 2 + b, (t >> 1) & 1, abort_flag, wait_ns)))) break;
       tc_fence_after();
       const uint32_t at = tbase + lanes + (kt * 2 + b) * N;
+      // the second half's load is under way while the first is reduced
+      uint32_t x[2][32];
+      static_assert(N == 64, "two halves of 32 columns");
+      tmem_ld32(at, x[0]);
+      tmem_ld32_nowait(at + 32, x[1]);
       if constexpr (MODE == SCAN_SCORES) {
         const int m = p.NV - t * N;      // real columns of the tile
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-          uint32_t x[32];
-          tmem_ld32(at + c0, x);
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tmem_wait_ld_tied(x[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
+          }
+          if (m >= N) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c0 + i < m) total = max_nan2(total, __uint_as_float(x[i]));
+            for (int i = 0; i < 32; ++i) total = max_nan2(total, __uint_as_float(x[h][i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * h + i < m) total = max_nan2(total, __uint_as_float(x[h][i]));
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
       } else {
-        const float4* l4 = reinterpret_cast<const float4*>(l2 + st * N);
-        const int4* m4 = reinterpret_cast<const int4*>(lim + st * N);
+        const float4* l4 = reinterpret_cast<const float4*>(l2 + sl * N);
+        const int4* m4 = reinterpret_cast<const int4*>(lim + sl * N);
         // this warp's highest key against the tile's first query
-        const bool masked = odd[st] || (p.causal && j0 + kt * ks::BM + (warp & 3) * 32 + 31 > lim[st * N]);
+        const bool masked = odd[sl] || (p.causal && j0 + kt * ks::BM + (warp & 3) * 32 + 31 > lim[sl * N]);
         float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-          uint32_t x[32];
-          tmem_ld32(at + c0, x);
-          if (c0 + 32 == N) {
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) {
+            tmem_wait_ld_tied(x[1]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
@@ -812,23 +862,23 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
           if (!masked) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 l = l4[c0 / 4 + i];
-              r0 += fast_ex2(fmaf(__uint_as_float(x[4 * i]), cs, -l.x));
-              r1 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 1]), cs, -l.y));
-              r2 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 2]), cs, -l.z));
-              r3 += fast_ex2(fmaf(__uint_as_float(x[4 * i + 3]), cs, -l.w));
+              const float4 l = l4[8 * h + i];
+              r0 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i]), cs, -l.x));
+              r1 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 1]), cs, -l.y));
+              r2 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 2]), cs, -l.z));
+              r3 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 3]), cs, -l.w));
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 l = l4[c0 / 4 + i];
-              const int4 m = m4[c0 / 4 + i];
+              const float4 l = l4[8 * h + i];
+              const int4 m = m4[8 * h + i];
               const float lv[4] = {l.x, l.y, l.z, l.w};
               const int mv[4] = {m.x, m.y, m.z, m.w};
               float ev[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                const float ex = fast_ex2(fmaf(__uint_as_float(x[4 * i + u]), cs, -lv[u]));
+                const float ex = fast_ex2(fmaf(__uint_as_float(x[h][4 * i + u]), cs, -lv[u]));
                 ev[u] = (lv[u] < INF || lv[u] != lv[u]) && j <= mv[u] ? ex : 0.f;
               }
               r0 += ev[0];
@@ -839,7 +889,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty + st);
+        if (lane == 0) mbar_arrive(l_empty + sl);
         total += (r0 + r1) + (r2 + r3);
       }
     }
@@ -900,21 +950,9 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
 #pragma unroll
     for (int u = 0; u < N / 32; ++u) nl[u] = lse_of(0, lane + 32 * u);
     for (int t = 0; t < T; ++t) {
-      const int st = t % NST, u2 = t / NST;
+      const int st = t % NST, u2 = t / NST, sl = t % NL;
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty + st, (u2 & 1) ^ 1, abort_flag, wait_ns))) break;
-      bool hide = false;
-#pragma unroll
-      for (int u = 0; u < N / 32; ++u) {
-        const int v = lane + 32 * u;
-        l2[st * N + v] = nl[u];
-        lim[st * N + v] = n - p.Nq + (t0 + t) * PT + v / p.G;
-        if (!p.causal) lim[st * N + v] = 0x7fffffff;
-        hide = hide || !(nl[u] < INF);
-        nl[u] = lse_of(t + 1, v);
-      }
-      hide = __any_sync(0xffffffffu, hide);
       if (lane == 0) {
-        odd[st] = hide;
         mbar_arrive_expect_tx(q_full + st, (uint32_t)KT * q_box * p.G * 128u);
 #pragma unroll
         for (int a = 0; a < KT; ++a)
@@ -923,6 +961,20 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
         par = (par & ~(1u << st)) | ((unsigned)(u2 & 1) << st);
       }
       __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait(l_empty + sl, ((t / NL) & 1) ^ 1, abort_flag, wait_ns))) break;
+      bool hide = false;
+#pragma unroll
+      for (int u = 0; u < N / 32; ++u) {
+        const int v = lane + 32 * u;
+        l2[sl * N + v] = nl[u];
+        lim[sl * N + v] = p.causal ? n - p.Nq + (t0 + t) * PT + v / p.G : 0x7fffffff;
+        hide = hide || !(nl[u] < INF);
+        nl[u] = lse_of(t + 1, v);
+      }
+      hide = __any_sync(0xffffffffu, hide);
+      if (lane == 0) odd[sl] = hide;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l_full + sl);
     }
     if (*abort_flag && lane == 0) {   // no TMA load may still be writing when the CTA exits
       for (int i = 0; i < NST; ++i)
@@ -930,9 +982,22 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     }
   } else {
     // ------------------------------------------------------------ queries, split by sign
-    constexpr int CPR = D / 8, STEP = Sh::NQW * 32;
+    constexpr int CPR = D / 8, STEP = Sh::NQW * 32, NX = N * CPR / STEP;
     const int qt = tid - Sh::W_Q * 32;
     const uint16_t* qg = static_cast<const uint16_t*>(p.q);
+    // this thread's 16-byte words of query tile t, one tile ahead
+    uint4 x[NX];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        const int f = i * STEP + qt, v = t * N + f / CPR;
+        const int vc = min(v, p.NV - 1);
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(
+                                  qg + (((size_t)s * p.Nq + vc / p.G) * p.Hq + g * p.G + vc % p.G) * D) + f % CPR);
+        x[i] = v < p.NV ? y : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    fetch(0);
     bool ok = true;
     int kk = 0;
     for (int t = 0; ok && t < T; ++t) {
@@ -941,14 +1006,12 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
         const int st = kk % NST;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, ((kk / NST) & 1) ^ 1, abort_flag, wait_ns)))) break;
         unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
-#pragma unroll 8
-        for (int f = qt; f < N * CPR; f += STEP) {
-          const int r = f / CPR, c = f % CPR, v = t * N + r;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (v < p.NV)
-            x = __ldg(reinterpret_cast<const uint4*>(qg + (((size_t)s * p.Nq + v / p.G) * p.Hq + g * p.G + v % p.G) * D) + c);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x, m == 0, bf16);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          const int f = i * STEP + qt, r = f / CPR, c = f % CPR;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x[i], m == 0, bf16);
         }
+        if (m == NK - 1 && t + 1 < T) fetch(t + 1);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full + st);
