@@ -45,13 +45,23 @@ constexpr int NWARP = W_KEY + NKEY;
 constexpr int THREADS = NWARP * 32;
 constexpr int MAXST = 8;
 constexpr int MAXN = kScanStreamVec;
-constexpr int PRE = 4;                     // tiles ahead that list entries are loaded
+constexpr int PRE = 6;                     // tiles ahead that list entries are loaded
 constexpr int SMEM_MAX = 225 * 1024;
 }  // namespace ks
 
 namespace {
 
 enum { SCAN_WEIGHTS = 0, SCAN_SCORES = 1 };
+
+// Tiles of codes in flight beside the one being widened: as many as the
+// shared memory beside 64 query vectors and the operand stages holds, at most PRE.
+template <int D, int KIND>
+__host__ __device__ constexpr int ks_ahead() {
+  const int code = ks::BM * kv_row_bytes<KIND>(D);
+  const int room = ks::SMEM_MAX - 3072 - 2 * ks::MAXN * D * 2 - (D <= 128 ? 2 : 1) * ks::BM * D * 2;
+  const int n = room / code - 1;
+  return n > ks::PRE ? ks::PRE : n;
+}
 
 // Shared memory of one instance: sizes that depend on N and the stage counts
 // are computed the same way on both sides.
@@ -72,10 +82,9 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   l.off_k = (2 * l.qb_bytes + 1023) / 1024 * 1024;
   const int room = ks::SMEM_MAX - 1024 - l.off_k - 2048;
   if (QUANT) {
-    // operand stages first (two; three for narrow heads), codes with what is left
+    // two operand stages (one for D 256), the code ring
     l.nst = D <= 128 ? 2 : 1;
-    l.ncs = (room - l.nst * l.tile) / l.code;
-    l.ncs = l.ncs > ks::MAXST ? ks::MAXST : l.ncs;
+    l.ncs = ks_ahead<D, KIND>() + 1;
   } else {
     l.nst = room / l.tile;
     l.nst = l.nst > ks::MAXST ? ks::MAXST : l.nst;
@@ -88,6 +97,18 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   l.total = l.off_l + 2 * ks::MAXN * 8 + 1024;
   return l;
 }
+
+// Position in a ring of n stages and the parity of its current phase.
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++st == n) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 // One CTA's walk over its share of the tiles.
 struct Walk {
@@ -235,7 +256,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
   // ---- this CTA's share of the triples
   long long total = 0;
   Walk w0;
-  long long mine = 0;
+  int mine = 0;   // tiles of this CTA's share
   {
     // tiles of all slices, THREADS slices at a time; then the slice that holds
     // this CTA's first tile
@@ -244,7 +265,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       long long start = 0;
       if (pass == 1) {
         start = total * blockIdx.x / gridDim.x;
-        mine = total * (blockIdx.x + 1) / gridDim.x - start;
+        mine = (int)(total * (blockIdx.x + 1) / gridDim.x - start);
         if (mine <= 0) return;
       }
       for (int base = 0; base < p.S; base += THREADS) {
@@ -312,64 +333,86 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
   if (warp < NEPI) {
     // ------------------------------------------------------------ reduction
     const uint32_t lanes = (uint32_t)warp << 21;   // tensor-memory lane base of this warp: 32 * warp, in bits 16 up
+    // What a thread needs of its key beside the products: loaded one tile
+    // ahead into one of two register sets, which the loop names in turn (a
+    // copy from one to the other would wait for the load).
+    struct Key {
+      int row;
+      unsigned short scale;
+      float old;
+    };
+    auto load_key = [&](const Walk& x, Key& a) {
+      const int j = x.t * BM + tid;
+      a.row = -1;
+      a.old = 0.f;
+      if (j < x.n) {
+        const int list = MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + x.s) : x.s;
+        a.row = __ldg(p.rows + (size_t)list * p.L + j);
+        if (MODE == SCAN_WEIGHTS && p.decay != 0.f) a.old = __ldg(p.out + ((size_t)x.s * p.Hkv + x.g) * p.L + j);
+      }
+    };
+    auto live = [&](const Key& a) { return a.row >= 0 && (long long)a.row < p.R; };
+    auto load_scale = [&](const Walk& x, Key& a) {
+      if (QUANT) a.scale = live(a) ? __ldg(p.k_scale + ((size_t)(a.row >> 6) * p.Hkv + x.g) * kPage + (a.row & 63)) : (unsigned short)0;
+    };
     Walk w = w0;
     int unit = 0;
-    // list entry (page) of the thread's key in the next tile, one tile ahead
-    auto entry = [&](const Walk& x) {
-      const int j = x.t * BM + tid;
-      if (j >= x.n) return -1;
-      const int list = MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + x.s) : x.s;
-      const int r = __ldg(p.rows + (size_t)list * p.L + j);
-      return (long long)r < p.R ? r : -1;
-    };
-    auto before = [&](const Walk& x) {   // the entry's accumulator
-      const int j = x.t * BM + tid;
-      if (MODE != SCAN_WEIGHTS || p.decay == 0.f || j >= x.n) return 0.f;
-      return __ldg(p.out + ((size_t)x.s * p.Hkv + x.g) * p.L + j);
-    };
-    int row = entry(w);
-    float old = before(w);
-    float scale = 1.f;
-    if (QUANT) scale = row >= 0 ? kv_scale_of(p.k_scale, row, w.g, p.Hkv) : 0.f;
-    bool ok = true;
-    for (long long k = 0; ok && k < mine; ++k) {
-      const int b = (int)(k & 1), qb = unit & 1;
+    // one tile: its key in cur; the next tile's goes to nxt
+    auto tile = [&](int k, Key& cur, Key& nxt) -> bool {
+      const int b = k & 1, qb = unit & 1;
       const bool first = k == 0 || w.t == 0;
       const bool last = k + 1 == mine || w.t + 1 == w.T;
       const int j = w.t * BM + tid;
       float* out = p.out + ((size_t)w.s * p.Hkv + w.g) * p.L;
       Walk nx = w;
-      int row_nx = -1;
-      float scale_nx = 1.f, old_nx = 0.f;
       if (k + 1 < mine) {
         ks_next<MODE>(p, nx);
-        row_nx = entry(nx);
-        old_nx = before(nx);
+        load_key(nx, nxt);
       }
-      if (first && !(ok = __all_sync(0xffffffffu, mbar_wait(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns)))) break;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (k >> 1) & 1, abort_flag, wait_ns)))) break;
+      if (first && !__all_sync(0xffffffffu, mbar_wait(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns))) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full + b, (k >> 1) & 1, abort_flag, wait_ns))) return false;
       tc_fence_after();
-      if (QUANT) scale_nx = row_nx >= 0 ? kv_scale_of(p.k_scale, row_nx, nx.g, p.Hkv) : 0.f;
-      const float* l2b = l2 + qb * MAXN;
-      const int* limb = lim + qb * MAXN;
+      const float4* l4 = reinterpret_cast<const float4*>(l2 + qb * MAXN);
+      const int4* m4 = reinterpret_cast<const int4*>(lim + qb * MAXN);
       // causal: every query sees positions up to n - Nq
       const bool masked = MODE == SCAN_WEIGHTS && p.causal && w.t * BM + BM - 1 > w.n - p.Nq;
-      const float cs = p.c * scale;
-      float r = MODE == SCAN_SCORES ? -INF : 0.f;
+      const float cs = QUANT ? p.c * __half2float(__ushort_as_half(cur.scale)) : p.c;
+      float r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) r[u] = MODE == SCAN_SCORES ? -INF : 0.f;
       for (int c0 = 0; c0 < N; c0 += 16) {
         uint32_t x[16];
         tmem_ld16(tbase + lanes + b * N + c0, x);
+        if (MODE == SCAN_SCORES) {
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          if (c0 + t >= p.NV) break;
-          const float v = __uint_as_float(x[t]);
-          if (MODE == SCAN_SCORES) {
-            r = max_nan2(r, v);
-          } else {
-            const float l = l2b[c0 + t];
-            const float e = fast_ex2(fmaf(v, cs, -l));
-            const bool see = l < INF || l != l;
-            r += see && (!masked || j <= limb[c0 + t]) ? e : 0.f;
+          for (int i = 0; i < 16; ++i) {
+            const float m = max_nan2(r[i & 3], __uint_as_float(x[i]));
+            r[i & 3] = c0 + i < p.NV ? m : r[i & 3];
+          }
+        } else {
+          // Columns without a query, and queries that saw nothing, have
+          // l = +inf and add nothing whatever their product.  Selections, not
+          // branches: a branch per column made this loop the kernel's bound
+          // (45.7 us where selections take 31, 4 x 16,384 entries).
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 l = l4[c0 / 4 + i];
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+            float e[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              e[u] = fast_ex2(fmaf(__uint_as_float(x[4 * i + u]), cs, -lv[u]));
+              e[u] = lv[u] == INF ? 0.f : e[u];
+            }
+            if (masked) {
+              const int4 m = m4[c0 / 4 + i];
+              e[0] = j <= m.x ? e[0] : 0.f;
+              e[1] = j <= m.y ? e[1] : 0.f;
+              e[2] = j <= m.z ? e[2] : 0.f;
+              e[3] = j <= m.w ? e[3] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r[u] += e[u];
           }
         }
       }
@@ -380,19 +423,25 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
         if (last) mbar_arrive(q_empty + qb);
       }
       if (MODE == SCAN_SCORES) {
-        if (j < w.n) out[j] = row >= 0 ? r : -INF;
+        if (j < w.n) out[j] = live(cur) ? max_nan2(max_nan2(r[0], r[1]), max_nan2(r[2], r[3])) : -INF;
         // past the sequence's blocks: the (slice, KV head)'s last tile fills the rest
         if (w.t + 1 == w.T)
           for (int f = w.n + tid; f < p.L; f += NEPI * 32) out[f] = -INF;
       } else if (j < w.n) {
-        const float add = row >= 0 ? r : 0.f;
-        out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
+        const float add = live(cur) ? (r[0] + r[1]) + (r[2] + r[3]) : 0.f;
+        out[j] = p.decay == 0.f ? add : fmaf(p.decay, cur.old, add);
       }
+      if (k + 1 < mine) load_scale(nx, nxt);
       if (last) ++unit;
       w = nx;
-      row = row_nx;
-      scale = scale_nx;
-      old = old_nx;
+      return true;
+    };
+    Key ka, kb;
+    load_key(w, ka);
+    load_scale(w, ka);
+    for (int k = 0; k < mine; k += 2) {
+      if (!tile(k, ka, kb)) break;
+      if (k + 1 < mine && !tile(k + 1, kb, ka)) break;
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issue
@@ -404,17 +453,18 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       Walk w = w0;
       int unit = 0;
       bool ok = true;
-      long long kk = 0;   // stage uses
-      for (long long k = 0; ok && k < mine; ++k) {
-        const int b = (int)(k & 1), qb = unit & 1;
+      Ring kr;
+      for (int k = 0; ok && k < mine; ++k) {
+        const int b = k & 1, qb = unit & 1;
         const bool first = k == 0 || w.t == 0, last = k + 1 == mine || w.t + 1 == w.T;
         if (first) ok = ks_poll(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns);
         ok = ok && ks_poll(s_empty + b, ((k >> 1) & 1) ^ 1, abort_flag, wait_ns);
 #pragma unroll
-        for (int m = 0; m < NK; ++m, ++kk) {
-          const int st = (int)(kk % NST);
-          ok = ok && ks_poll(k_full + st, (kk / NST) & 1, abort_flag, wait_ns);
+        for (int m = 0; m < NK; ++m) {
+          const int st = kr.st;
+          ok = ok && ks_poll(k_full + st, kr.ph, abort_flag, wait_ns);
           if (!ok) break;
+          kr.next(NST);
           tc_fence_after();
           fence_proxy_async_smem();   // the stage's cp.async copies arrived by themselves
           const uint64_t a = sdesc_at(dK, st * ly.tile), q = sdesc_at(dQ, qb * ly.qb_bytes + m * KT * qatom);
@@ -438,7 +488,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
   } else if (warp == W_Q) {
     // ------------------------------------------------------------ queries
     Walk w = w0;
-    long long left = mine;
+    int left = mine;
     constexpr int CPR = D / 8;   // 16-byte chunks of a query vector
     for (int unit = 0; left > 0; ++unit) {
       const int qb = unit & 1;
@@ -460,8 +510,8 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
         }
       }
       if (MODE == SCAN_WEIGHTS) {
-        for (int v = lane; v < p.NV; v += 32) {
-          const float l = __ldg(p.lse + ((size_t)w.s * p.Nq + v / p.G) * p.Hq + w.g * p.G + v % p.G);
+        for (int v = lane; v < N; v += 32) {
+          const float l = v < p.NV ? __ldg(p.lse + ((size_t)w.s * p.Nq + v / p.G) * p.Hq + w.g * p.G + v % p.G) : -INF;
           l2[qb * MAXN + v] = l == -INF ? INF : l * kLog2e;
           lim[qb * MAXN + v] = w.n - p.Nq + v / p.G;
         }
@@ -485,20 +535,20 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
     auto list_of_slice = [&](const Walk& x) {
       return MODE == SCAN_SCORES && p.slice_seq ? (size_t)max(__ldg(p.slice_seq + x.s), 0) : (size_t)x.s;
     };
-    auto entry = [&](const Walk& x, int e) {   // row (page) of key e of the tile, -1: none
+    auto entry = [&](const Walk& x, int e) {   // list entry (page) of key e of the tile as it stands, -1 past the end
       const int j = x.t * BM + e;
-      if (j >= x.n) return -1;
-      const int r = __ldg(p.rows + list_of_slice(x) * p.L + j);
-      return r >= 0 && (long long)r < p.R ? r : -1;
+      return j < x.n ? __ldg(p.rows + list_of_slice(x) * p.L + j) : -1;
     };
+    auto row_of = [&](int r) { return r >= 0 && (long long)r < p.R ? r : -1; };
     if constexpr (!QUANT) {
       constexpr int CPR = D / 8;
       unsigned tma_pend = 0, tma_par = 0;
-      // list entries PRE tiles ahead: a tile's share of HBM time is shorter
-      // than the latency of a list load
+      // List entries PRE tiles ahead (a tile's share of HBM time is shorter
+      // than the latency of a list load), in register sets that the unrolled
+      // loop names in turn.
       int nx0[PRE], nx1[PRE];
       Walk wp = w;
-      long long kp = 0;
+      int kp = 0;
       auto fetch = [&](int& a, int& b) {
         if (kp < mine) {
           a = entry(wp, half * 64 + lane);
@@ -508,48 +558,48 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       };
 #pragma unroll
       for (int i = 0; i < PRE; ++i) fetch(nx0[i], nx1[i]);
-      long long kk = 0;
+      Ring kr;
       bool ok = true;
-      for (long long k = 0; ok && k < mine; ++k) {
-        const int r0 = nx0[0], r1 = nx1[0], g = w.g;
+      for (int k0 = 0; ok && k0 < mine; k0 += PRE) {
 #pragma unroll
-        for (int i = 0; i + 1 < PRE; ++i) {
-          nx0[i] = nx0[i + 1];
-          nx1[i] = nx1[i + 1];
-        }
-        fetch(nx0[PRE - 1], nx1[PRE - 1]);
-        if (k + 1 < mine) ks_next<MODE>(p, w);
-        const int base = __shfl_sync(0xffffffffu, r0, 0);
-        const bool run = __all_sync(0xffffffffu, r0 >= 0 && r0 == base + lane && r1 == base + 32 + lane) && tma_ok;
+        for (int i = 0; i < PRE; ++i) {
+          if (!ok || k0 + i >= mine) break;
+          const int r0 = row_of(nx0[i]), r1 = row_of(nx1[i]), g = w.g;
+          const int base = __shfl_sync(0xffffffffu, r0, 0);
+          const bool run = __all_sync(0xffffffffu, r0 >= 0 && r0 == base + lane && r1 == base + 32 + lane) && tma_ok;
 #pragma unroll
-        for (int m = 0; m < NK; ++m, ++kk) {
-          const int st = (int)(kk % NST), u = (int)(kk / NST);
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, (u & 1) ^ 1, abort_flag, wait_ns)))) break;
-          unsigned char* dst = sm + ly.off_k + st * ly.tile + half * 64 * 128;
-          if (run) {
-            if (quarter == 0 && lane == 0) {
-              mbar_arrive_expect_tx(k_full + st, 64 * D * 2);
+          for (int m = 0; m < NK; ++m) {
+            const int st = kr.st;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, kr.ph ^ 1u, abort_flag, wait_ns)))) break;
+            unsigned char* dst = sm + ly.off_k + st * ly.tile + half * 64 * 128;
+            if (run) {
+              if (quarter == 0 && lane == 0) {
+                mbar_arrive_expect_tx(k_full + st, 64 * D * 2);
 #pragma unroll
-              for (int a = 0; a < KT; ++a) tma_load_3d(dst + a * ATOM, m ? &t1 : &t0, a * 64, g, base, k_full + st);
-              tma_pend |= 1u << st;
-              tma_par = (tma_par & ~(1u << st)) | ((unsigned)(u & 1) << st);
+                for (int a = 0; a < KT; ++a) tma_load_3d(dst + a * ATOM, m ? &t1 : &t0, a * 64, g, base, k_full + st);
+                tma_pend |= 1u << st;
+                tma_par = (tma_par & ~(1u << st)) | (kr.ph << st);
+              } else {
+                mbar_arrive(k_full + st);
+              }
             } else {
-              mbar_arrive(k_full + st);
-            }
-          } else {
-            const char* src = static_cast<const char*>(p.k[m]);
+              const char* src = static_cast<const char*>(p.k[m]) + (size_t)g * (D * 2);
+              const size_t pitch = (size_t)p.Hkv * (D * 2);
 #pragma unroll
-            for (int it = 0; it < 16 * CPR / 32; ++it) {
-              const int f = it * 32 + lane;
-              const int e = quarter * 16 + f / CPR, c = f % CPR;   // row of the half, chunk
-              const int ra = __shfl_sync(0xffffffffu, r0, e & 31), rb = __shfl_sync(0xffffffffu, r1, e & 31);
-              const int r = e < 32 ? ra : rb;
-              const bool okr = r >= 0;
-              const size_t go = ((size_t)(okr ? r : 0) * p.Hkv + g) * (D * 2) + c * 16;
-              cp_async16(dst + (c >> 3) * ATOM + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + go, okr);
+              for (int it = 0; it < 16 * CPR / 32; ++it) {
+                const int f = it * 32 + lane;
+                const int e = quarter * 16 + f / CPR, c = f % CPR;   // row of the half, chunk
+                // a quarter's 16 rows lie in one of the two registers
+                const int r = __shfl_sync(0xffffffffu, quarter < 2 ? r0 : r1, e & 31);
+                cp_async16(dst + (c >> 3) * ATOM + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + (r >= 0 ? r : 0) * pitch + c * 16,
+                           r >= 0);
+              }
+              cp_async_mbar_arrive_noinc(k_full + st);
             }
-            cp_async_mbar_arrive_noinc(k_full + st);
+            kr.next(NST);
           }
+          fetch(nx0[i], nx1[i]);
+          if (k0 + i + 1 < mine) ks_next<MODE>(p, w);
         }
       }
       cp_async_wait_all();
@@ -562,11 +612,11 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       // own 16-byte chunks, which lie lane by lane in the code ring
       constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, NIT = 16 * CPR / 32;
       static_assert(16 * CPR % 32 == 0, "a warp's chunks fill its lanes");
-      const int NCS = ly.ncs;
+      constexpr int AHEAD = ks_ahead<D, KIND>(), NCS = AHEAD + 1;
       unsigned char* ring = sm + ly.off_c + kw * 16 * CB;
       Walk wi = w, wp = w;                          // the copies' walk, NCS tiles ahead; the list entries', PRE more
       int nx[PRE];                                  // rows of the next tiles to copy, lanes 0-15
-      long long ki = 0, kp = 0;
+      int ki = 0, kp = 0, slot = 0;
       auto fetch = [&](int& a) {
         if (kp < mine) {
           a = entry(wp, kw * 16 + (lane & 15));
@@ -575,47 +625,39 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       };
 #pragma unroll
       for (int i = 0; i < PRE; ++i) fetch(nx[i]);
-      auto issue = [&]() {
-        const int row = nx[0], g = wi.g;
+      // the copies of tile ki, whose list entries are in `set`; one group, empty past the share
+      auto issue = [&](int& set) {
+        if (ki < mine) {
+          const int row = row_of(set), g = wi.g;
+          unsigned char* dst = ring + slot * ly.code;
+          if (++slot == NCS) slot = 0;
 #pragma unroll
-        for (int i = 0; i + 1 < PRE; ++i) nx[i] = nx[i + 1];
-        fetch(nx[PRE - 1]);
-        if (ki + 1 < mine) ks_next<MODE>(p, wi);
-        unsigned char* dst = ring + (ki % NCS) * ly.code;
-#pragma unroll
-        for (int it = 0; it < NIT; ++it) {
-          const int f = it * 32 + lane, e = f / CPR, c = f % CPR;
-          const int r = __shfl_sync(0xffffffffu, row, e);
-          const bool okr = r >= 0;
-          cp_async16(dst + f * 16, static_cast<const char*>(p.k[0]) + ((size_t)(okr ? r : 0) * p.Hkv + g) * CB + c * 16, okr);
+          for (int it = 0; it < NIT; ++it) {
+            const int f = it * 32 + lane, e = f / CPR, c = f % CPR;
+            const int r = __shfl_sync(0xffffffffu, row, e);
+            const bool okr = r >= 0;
+            cp_async16(dst + f * 16, static_cast<const char*>(p.k[0]) + ((size_t)(okr ? r : 0) * p.Hkv + g) * CB + c * 16, okr);
+          }
+          fetch(set);
+          if (++ki < mine) ks_next<MODE>(p, wi);
         }
-        ++ki;
-      };
-      for (int i = 0; i < NCS - 1; ++i) {
-        if (ki < mine) issue();
         cp_async_commit();
-      }
-      bool ok = true;
-      for (long long k = 0; ok && k < mine; ++k) {
-        // copies of tile k have landed once at most NCS - 2 later groups are pending
-        switch (NCS) {
-          case 8: cp_async_wait<6>(); break;
-          case 7: cp_async_wait<5>(); break;
-          case 6: cp_async_wait<4>(); break;
-          case 5: cp_async_wait<3>(); break;
-          case 4: cp_async_wait<2>(); break;
-          case 3: cp_async_wait<1>(); break;
-          default: cp_async_wait<0>(); break;
-        }
+      };
+      // one tile: widen it, issue the copies of the tile AHEAD later
+      Ring kr;
+      int rd = 0;
+      auto tile = [&](int& set) -> bool {
+        // copies of this tile have landed once at most AHEAD - 1 later groups are pending
+        cp_async_wait<AHEAD - 1>();
         uint4 cw[NIT];
-        const unsigned char* src = ring + (k % NCS) * ly.code;
+        const unsigned char* src = ring + rd * ly.code;
+        if (++rd == NCS) rd = 0;
 #pragma unroll
         for (int it = 0; it < NIT; ++it) cw[it] = *reinterpret_cast<const uint4*>(src + (it * 32 + lane) * 16);
-        // the ring's next slot is the one tile k - 1 left
-        if (ki < mine) issue();
-        cp_async_commit();
-        const int st = (int)(k % NST), u = (int)(k / NST);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, (u & 1) ^ 1, abort_flag, wait_ns)))) break;
+        issue(set);   // into the slot that the tile before this one left
+        const int st = kr.st;
+        if (!__all_sync(0xffffffffu, mbar_wait(k_empty + st, kr.ph ^ 1u, abort_flag, wait_ns))) return false;
+        kr.next(NST);
         unsigned char* dst = sm + ly.off_k + st * ly.tile;
         constexpr int W = KvChunk<KIND>::N / 8;     // 16-byte words a chunk widens to
 #pragma unroll
@@ -630,6 +672,18 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + st);
+        return true;
+      };
+      static_assert(AHEAD <= PRE, "the list entries of the copies issued first");
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) issue(nx[i]);
+      bool ok = true;
+      for (int k0 = 0; ok && k0 < mine; k0 += PRE) {
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) {
+          if (!ok || k0 + i >= mine) break;
+          ok = tile(nx[(i + AHEAD) % PRE]);
+        }
       }
       cp_async_wait_all();
     }
@@ -649,86 +703,98 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 // Many query vectors (prompts): a CTA keeps its keys in shared memory and the
 // queries stream past them.
 //
-// For weights the exponential bounds it (16 a clock and SM, where the tensor
-// core forms 64 products of D = 128 in that time), for scores the tensor core.  A CTA owns
-// NT tiles of 128 keys, so each staged query tile is used NT times; one
-// warpgroup reduces each key tile (thread = key, as above), with two
-// accumulators per key tile so that the products of the next query tile are
-// formed meanwhile.  Two CTAs share an SM where they fit (weights, D <= 128):
-// one's key gather and waits lie under the other's exponentials.
+// Per 128 x 128 x 128 tile the tensor core takes 512 clocks and the
+// exponentials (32 a clock and SM) as many; a staged query tile, 256 rows of
+// 128 bytes to the TMA unit, takes about three times that.  So a CTA owns up to
+// NT = 4 tiles of 128 keys, each query tile is used for all of them, and one
+// warpgroup reduces each key tile (thread = key, as above) while the tensor core is at the
+// others.  The key tiles of a CTA are nb apart, so that under a causal limit
+// every CTA has early and late ones.
+// Scores (two stages per query tile, for max(q, 0) and min(q, 0)) keep both
+// bounds of one key tile and two CTAs per SM; a CTA walks several slices,
+// and stages the bounds again only where the slice is of another sequence.
 //   warps 0 .. 4 NT - 1   gather (and widen) the keys, then the reduction
 //   then                  MMA issue; queries: TMA boxes of whole queries
-//                         (weights), or loads that split q into max(q, 0) and
-//                         min(q, 0) tiles (scores, two per query tile)
+//                         (weights), or loads split by sign (scores)
 namespace kp {
 template <int D, int MODE>
 struct Shape {
-  static constexpr int NT = MODE == SCAN_SCORES ? 1 : 2;                  // key tiles
-  static constexpr int N = 64;                                            // query vectors per tile
-  static constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;                  // stages per query tile
+  static constexpr bool SC = MODE == SCAN_SCORES;
+  static constexpr int NT = SC ? 1 : D == 256 ? 2 : 4;      // key tiles
+  static constexpr int N = SC || D == 256 ? 64 : 128;       // query vectors per tile
+  static constexpr int NB = SC || D == 256 ? 2 : 1;         // accumulators per key tile
+  static constexpr int NK = SC ? 2 : 1;                     // stages per query tile
   static constexpr int NST = D == 64 ? 4 : 2;
-  static constexpr int NL = 4;                                            // query tiles whose lse are on chip
-  static constexpr int CTAS = D <= 128 ? 2 : 1;                           // per SM
+  static constexpr int NL = 4;                              // query tiles whose lse are on chip
+  static constexpr int CTAS = SC && D <= 128 ? 2 : 1;       // per SM
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
   static constexpr int QST = N * D * 2;               // one query stage
-  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = MODE == SCAN_SCORES ? 4 : 1;
+  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = SC ? 4 : 1;
   static constexpr int THREADS = (W_Q + NQW) * 32;
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
-  static constexpr int NBAR = 1 + 2 * NST + 4 * NT + 1 + 2 * NL;
+  static constexpr int NBAR = 1 + 2 * NST + 2 * NB * NT + 1 + 2 * NL;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NL][N] lse, [NL][N] limits, [NL] flags
-  static constexpr int OFF_IDX = OFF_L + (MODE == SCAN_WEIGHTS ? NL * N * 8 + NL * 4 : 0);
+  static constexpr int OFF_IDX = OFF_L + (SC ? 0 : NL * N * 8 + NL * 4);
   static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
   static constexpr int SMEM = USED + 1024;
-  static constexpr uint32_t COLS = NT * 2 * N;
+  static constexpr uint32_t COLS = NT * NB * N;
   static_assert(COLS * CTAS <= 512 && (COLS & (COLS - 1)) == 0, "tensor memory");
-  static_assert((SMEM + 1024) * CTAS <= 227 * 1024 + 1024, "shared memory");
+  static_assert((SMEM + 1024) * CTAS <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");
 };
 }  // namespace kp
 
+struct PromptPlan {
+  int PT, q_box;    // weights: queries per tile, and per TMA box
+  int nb;           // batches of key tiles per (slice, KV head); key tile kt of batch j is tile j + kt * nb
+  int sc, chunks;   // slices per CTA, chunks of slices
+};
+
 template <int D, int MODE, int KIND>
 __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, MODE>::CTAS))
-    keyscan_prompt_kernel(const KeyScanParams p, int PT, int q_box, const __grid_constant__ CUtensorMap tq) {
+    keyscan_prompt_kernel(const KeyScanParams p, const PromptPlan pl, const __grid_constant__ CUtensorMap tq) {
   using Sh = kp::Shape<D, MODE>;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
-  constexpr int NT = Sh::NT, N = Sh::N, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64, KEYS = NT * ks::BM;
+  constexpr int NT = Sh::NT, N = Sh::N, NB = Sh::NB, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
+  constexpr int BM = ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* key_full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t* q_full = key_full + 1;
   uint64_t* q_empty = q_full + NST;
-  uint64_t* s_full = q_empty + NST;      // [NT][2]
-  uint64_t* s_empty = s_full + 2 * NT;   // [NT][2]
-  uint64_t* drain = s_empty + 2 * NT;
+  uint64_t* s_full = q_empty + NST;      // [NT][NB]
+  uint64_t* s_empty = s_full + NB * NT;  // [NT][NB]
+  uint64_t* drain = s_empty + NB * NT;
   uint64_t* l_full = drain + 1;          // [NL] lse, limits and flag of a query tile
   uint64_t* l_empty = l_full + NL;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + Sh::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::OFF_MISC + 4);
   float* l2 = reinterpret_cast<float*>(sm + Sh::OFF_L);
   int* lim = reinterpret_cast<int*>(l2 + NL * N);
-  int* odd = lim + NL * N;              // a column of the stage's tile adds nothing, whatever its product
+  int* odd = lim + NL * N;               // a column of the tile adds nothing, whatever its product
   int* idx = reinterpret_cast<int*>(sm + Sh::OFF_IDX);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.z, g = blockIdx.y, j0 = blockIdx.x * KEYS;
   const bool bf16 = p.q_bf16 != 0;
   const unsigned long long wait_ns = p.wait_ns;
-  const int n = ks_entries<MODE>(p, s);
-  float* out = p.out + ((size_t)s * p.Hkv + g) * p.L;
-  if (j0 >= n) {   // no such keys; blocks past the sequence score -inf
-    if (MODE == SCAN_SCORES)
-      for (int j = j0 + tid; j < min(j0 + KEYS, p.L); j += Sh::THREADS) out[j] = -INF;
-    return;
-  }
-  // query tiles of PT queries (weights; N vectors for scores); a causal CTA
-  // starts at the first query that sees its first key
-  int t0 = 0;
-  const int nt = MODE == SCAN_SCORES ? (p.NV + N - 1) / N : (p.Nq + PT - 1) / PT;
-  if (MODE == SCAN_WEIGHTS && p.causal) t0 = min(nt, max(0, j0 - (n - p.Nq)) / PT);
-  const int T = nt - t0;
+  // (KV head, slice chunk) fastest: neighbouring CTAs read the same rows' heads
+  const int per = p.Hkv * pl.chunks;
+  const int batch = blockIdx.x / per, g = blockIdx.x % per % p.Hkv, chunk = blockIdx.x % per / p.Hkv;
+  const int s_lo = chunk * pl.sc, s_hi = min(s_lo + pl.sc, p.S);
+  const int nt = MODE == SCAN_SCORES ? (p.NV + N - 1) / N : (p.Nq + pl.PT - 1) / pl.PT;
+  auto key0 = [&](int kt) { return (batch + kt * pl.nb) * BM; };   // first key of key tile kt
+  // A causal key tile starts at the first query tile that sees its first key,
+  // the CTA at its first key tile's; nt where the slice has no such keys.
+  auto first_tile = [&](int kt, int n) {
+    const long long j = (long long)batch * BM + (long long)kt * pl.nb * BM;
+    if (j >= n) return nt;
+    return MODE == SCAN_WEIGHTS && p.causal ? min(nt, max(0, (int)j - (n - p.Nq)) / pl.PT) : 0;
+  };
+  if (MODE == SCAN_WEIGHTS && first_tile(0, ks_entries<MODE>(p, s_lo)) == nt && p.decay == 1.f) return;   // nothing to add
+  if (MODE == SCAN_WEIGHTS && key0(0) >= ks_entries<MODE>(p, s_lo)) return;
 
   if (tid == 0) {
     mbar_init(key_full, Sh::NEPI * 32);
@@ -740,7 +806,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
       mbar_init(l_full + i, 1);
       mbar_init(l_empty + i, Sh::NEPI);
     }
-    for (int i = 0; i < 2 * NT; ++i) {
+    for (int i = 0; i < NB * NT; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 4);
     }
@@ -752,12 +818,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     tmem_alloc(tmem_holder, Sh::COLS);
     tmem_relinquish();
   }
-  const size_t list = MODE == SCAN_SCORES && p.slice_seq ? (size_t)__ldg(p.slice_seq + s) : (size_t)s;
-  for (int e = tid; e < KEYS; e += Sh::THREADS) {
-    const int r = j0 + e < n ? __ldg(p.rows + list * p.L + j0 + e) : -1;
-    idx[e] = r >= 0 && (long long)r < p.R ? r : -1;
-  }
-  if (MODE == SCAN_WEIGHTS && q_box * p.G < N) {
+  if (MODE == SCAN_WEIGHTS && pl.q_box * p.G < N) {
     // rows of a query tile that no box writes
     for (int f = tid; f < NST * Sh::QST / 16; f += Sh::THREADS)
       reinterpret_cast<uint4*>(sm + Sh::OFF_Q)[f] = make_uint4(0u, 0u, 0u, 0u);
@@ -767,119 +828,145 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  // the list (page table row) of a slice
+  auto list_of_slice = [&](int s) { return MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + s) : s; };
 
   if (warp < Sh::NEPI) {
-    // ------------------------------------------------------------ keys
-    if constexpr (QUANT) {
-      constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, W = KvChunk<KIND>::N / 8;
-#pragma unroll 4
-      for (int f = tid; f < KEYS * CPR; f += KEYS) {
-        const int e = f / CPR, c = f % CPR, r = idx[e];
-        uint4 cw = make_uint4(0u, 0u, 0u, 0u), o[W];
-        if (r >= 0)
-          cw = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k[0]) + ((size_t)r * p.Hkv + g) * CB) + c);
-        widen_chunk<KIND>(cw, bf16, o);
-        unsigned char* dst = sm + (e >> 7) * Sh::KMAT + (e & 127) * 128;
-#pragma unroll
-        for (int x = 0; x < W; ++x) {
-          const int cc = c * W + x;
-          *reinterpret_cast<uint4*>(dst + (cc >> 3) * Sh::ATOM + (((cc & 7) ^ (e & 7)) << 4)) = o[x];
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(key_full);
-    } else {
-      constexpr int CPR = D / 8;
-#pragma unroll
-      for (int m = 0; m < NK; ++m) {
-        const char* src = static_cast<const char*>(p.k[m]);
-#pragma unroll 8
-        for (int f = tid; f < KEYS * CPR; f += KEYS) {
-          const int e = f / CPR, c = f % CPR, r = idx[e];
-          const size_t go = ((size_t)max(r, 0) * p.Hkv + g) * (D * 2) + c * 16;
-          cp_async16(sm + ((e >> 7) * NK + m) * Sh::KMAT + (c >> 3) * Sh::ATOM + (e & 127) * 128 + (((c & 7) ^ (e & 7)) << 4),
-                     src + go, r >= 0);
-        }
-      }
-      cp_async_mbar_arrive_noinc(key_full);
-    }
-    // ------------------------------------------------------------ reduction
+    // ------------------------------------------------------------ keys and reduction
     const int kt = warp >> 2;                              // this warpgroup's key tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const int e = kt * ks::BM + (tid & 127), j = j0 + e;
-    const int row = idx[e];
-    const float cs = QUANT && row >= 0 ? p.c * kv_scale_of(p.k_scale, row, g, p.Hkv) : p.c;
-    float old = 0.f;
-    if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldg(out + j);
-    float total = MODE == SCAN_SCORES ? -INF : 0.f;
+    const int e = tid & 127;
+    const long long jj = (long long)batch * BM + (long long)kt * pl.nb * BM + e;
+    const int j = jj < p.L ? (int)jj : p.L;                // past every slice's entries where there is none
+    int* my_idx = idx + kt * BM;
+    unsigned char* kdst = sm + kt * NK * Sh::KMAT;
+    int loaded = -1, row = -1;
+    float cs = p.c;
+    int round = 0, lround = 0;                             // accumulators and lse slots used so far
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      const int b = t & 1, sl = t % NL;
-      if (MODE == SCAN_WEIGHTS &&
-          !(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (t / NL) & 1, abort_flag, wait_ns))))
-        break;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + kt * 2 + b, (t >> 1) & 1, abort_flag, wait_ns)))) break;
-      tc_fence_after();
-      const uint32_t at = tbase + lanes + (kt * 2 + b) * N;
-      // the second half's load is under way while the first is reduced
-      uint32_t x[2][32];
-      static_assert(N == 64, "two halves of 32 columns");
-      tmem_ld32(at, x[0]);
-      tmem_ld32_nowait(at + 32, x[1]);
-      if constexpr (MODE == SCAN_SCORES) {
-        const int m = p.NV - t * N;      // real columns of the tile
+    for (int s = s_lo; ok && s < s_hi; ++s) {
+      const int n = ks_entries<MODE>(p, s);
+      const int t0 = first_tile(0, n), T = nt - t0, mine = first_tile(kt, n) - t0;
+      float* out = p.out + ((size_t)s * p.Hkv + g) * p.L;
+      if (MODE == SCAN_SCORES && T == 0) {                 // no such blocks
+        if (j < p.L) out[j] = -INF;
+        continue;
+      }
+      const int list = list_of_slice(s);
+      if (list != loaded) {
+        // This warpgroup's key tile: its products of earlier slices have all
+        // been read, so nothing else uses the tile.  For scores every page of
+        // the table is staged, since later slices may see more of them.
+        loaded = list;
+        row = j < (MODE == SCAN_SCORES ? p.L : n) ? __ldg(p.rows + (size_t)list * p.L + j) : -1;
+        row = row >= 0 && (long long)row < p.R ? row : -1;
+        my_idx[e] = row;
+        named_barrier(1 + kt, 128);
+        if constexpr (QUANT) {
+          constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, W = KvChunk<KIND>::N / 8;
+#pragma unroll 4
+          for (int f = e; f < BM * CPR; f += BM) {
+            const int k = f / CPR, c = f % CPR, r = my_idx[k];
+            uint4 o[W];
+            const uint4 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k[0]) + ((size_t)max(r, 0) * p.Hkv + g) * CB) + c);
+            widen_chunk<KIND>(r >= 0 ? y : make_uint4(0u, 0u, 0u, 0u), bf16, o);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            tmem_wait_ld_tied(x[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
+            for (int x = 0; x < W; ++x) {
+              const int cc = c * W + x;
+              *reinterpret_cast<uint4*>(kdst + (cc >> 3) * Sh::ATOM + k * 128 + (((cc & 7) ^ (k & 7)) << 4)) = o[x];
+            }
           }
-          if (m >= N) {
+          fence_proxy_async_smem();
+          mbar_arrive(key_full);
+          if (row >= 0) cs = p.c * kv_scale_of(p.k_scale, row, g, p.Hkv);
+        } else {
+          constexpr int CPR = D / 8;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) total = max_nan2(total, __uint_as_float(x[h][i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * h + i < m) total = max_nan2(total, __uint_as_float(x[h][i]));
+          for (int m = 0; m < NK; ++m) {
+            const char* src = static_cast<const char*>(p.k[m]) + (size_t)g * (D * 2);
+            const size_t pitch = (size_t)p.Hkv * (D * 2);
+#pragma unroll 8
+            for (int f = e; f < BM * CPR; f += BM) {
+              const int k = f / CPR, c = f % CPR, r = my_idx[k];
+              cp_async16(kdst + m * Sh::KMAT + (c >> 3) * Sh::ATOM + k * 128 + (((c & 7) ^ (k & 7)) << 4),
+                         src + max(r, 0) * pitch + c * 16, r >= 0);
+            }
+          }
+          cp_async_mbar_arrive_noinc(key_full);
+        }
+      }
+      float old = 0.f;
+      if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldg(out + j);
+      float total = MODE == SCAN_SCORES ? -INF : 0.f;
+      for (int t = 0; t < T; ++t) {
+        const int sl = lround % NL;
+        if (MODE == SCAN_WEIGHTS) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (lround / NL) & 1, abort_flag, wait_ns)))) break;
+          ++lround;
+          if (t < mine) {   // these queries see none of the key tile
+            __syncwarp();
+            if (lane == 0) mbar_arrive(l_empty + sl);
+            continue;
           }
         }
-      } else {
+        const int b = round % NB;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + kt * NB + b, (round / NB) & 1, abort_flag, wait_ns)))) break;
+        ++round;
+        tc_fence_after();
+        const uint32_t at = tbase + lanes + (kt * NB + b) * N;
+        const int m = p.NV - t * N;      // scores: real columns of the tile
         const float4* l4 = reinterpret_cast<const float4*>(l2 + sl * N);
         const int4* m4 = reinterpret_cast<const int4*>(lim + sl * N);
         // this warp's highest key against the tile's first query
-        const bool masked = odd[sl] || (p.causal && j0 + kt * ks::BM + (warp & 3) * 32 + 31 > lim[sl * N]);
+        const bool masked = MODE == SCAN_WEIGHTS && (odd[sl] || (p.causal && key0(kt) + (warp & 3) * 32 + 31 > lim[sl * N]));
         float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+        // 32 columns at a time, the next ones' load under way meanwhile
+        uint32_t x[2][32];
+        tmem_ld32(at, x[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            tmem_wait_ld_tied(x[1]);
+        for (int c = 0; c < N / 32; ++c) {
+          uint32_t(&y)[32] = x[c & 1];
+          if (c > 0) tmem_wait_ld_tied(y);
+          if (c + 1 < N / 32) {
+            tmem_ld32_nowait(at + 32 * (c + 1), x[(c + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty + kt * 2 + b);
+            if (lane == 0) mbar_arrive(s_empty + kt * NB + b);
           }
-          if (!masked) {
+          if constexpr (MODE == SCAN_SCORES) {
+            if (m >= N) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) total = max_nan2(total, __uint_as_float(y[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float z = max_nan2(total, __uint_as_float(y[i]));
+                total = 32 * c + i < m ? z : total;
+              }
+            }
+          } else if (!masked) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 l = l4[8 * h + i];
-              r0 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i]), cs, -l.x));
-              r1 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 1]), cs, -l.y));
-              r2 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 2]), cs, -l.z));
-              r3 += fast_ex2(fmaf(__uint_as_float(x[h][4 * i + 3]), cs, -l.w));
+              const float4 l = l4[8 * c + i];
+              r0 += fast_ex2(fmaf(__uint_as_float(y[4 * i]), cs, -l.x));
+              r1 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 1]), cs, -l.y));
+              r2 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 2]), cs, -l.z));
+              r3 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 3]), cs, -l.w));
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 l = l4[8 * h + i];
-              const int4 m = m4[8 * h + i];
+              const float4 l = l4[8 * c + i];
+              const int4 q = m4[8 * c + i];
               const float lv[4] = {l.x, l.y, l.z, l.w};
-              const int mv[4] = {m.x, m.y, m.z, m.w};
+              const int mv[4] = {q.x, q.y, q.z, q.w};
               float ev[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                const float ex = fast_ex2(fmaf(__uint_as_float(x[h][4 * i + u]), cs, -lv[u]));
-                ev[u] = (lv[u] < INF || lv[u] != lv[u]) && j <= mv[u] ? ex : 0.f;
+                const float ex = fast_ex2(fmaf(__uint_as_float(y[4 * i + u]), cs, -lv[u]));
+                ev[u] = lv[u] == INF ? 0.f : ex;
+                ev[u] = j <= mv[u] ? ev[u] : 0.f;
               }
               r0 += ev[0];
               r1 += ev[1];
@@ -888,50 +975,77 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(l_empty + sl);
-        total += (r0 + r1) + (r2 + r3);
+        if (MODE == SCAN_WEIGHTS) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(l_empty + sl);
+          total += (r0 + r1) + (r2 + r3);
+        }
       }
-    }
-    if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
-    if (j < n) {
-      if (MODE == SCAN_SCORES) {
-        out[j] = row >= 0 ? total : -INF;
-      } else {
-        const float add = row >= 0 ? total : 0.f;
-        out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
+      if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
+      if (j < n) {
+        if (MODE == SCAN_SCORES) {
+          out[j] = row >= 0 ? total : -INF;
+        } else {
+          const float add = row >= 0 ? total : 0.f;
+          out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
+        }
+      } else if (MODE == SCAN_SCORES && j < p.L) {
+        out[j] = -INF;
       }
-    } else if (MODE == SCAN_SCORES && j < p.L) {
-      out[j] = -INF;
     }
   } else if (warp == Sh::W_MMA) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
-      const uint32_t id = make_idesc_f16(ks::BM, N, bf16, false);
+      const uint32_t id = make_idesc_f16(BM, N, bf16, false);
       const uint64_t dK = sdesc_sw128(smem_u32(sm), 16, 1024);
       const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
-      bool ok = ks_poll(key_full, 0, abort_flag, wait_ns);
-      fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
-      int kk = 0;
-      for (int t = 0; ok && t < T; ++t) {
-        const int b = t & 1;
+      bool ok = true;
+      int loaded = -1, loads = 0, rounds[NT];
 #pragma unroll
-        for (int m = 0; m < NK; ++m, ++kk) {
-          const int st = kk % NST;
-          ok = ok && ks_poll(q_full + st, (kk / NST) & 1, abort_flag, wait_ns);
-          for (int kt = 0; ok && kt < NT; ++kt) {
-            if (m == 0) ok = ks_poll(s_empty + kt * 2 + b, ((t >> 1) & 1) ^ 1, abort_flag, wait_ns);
+      for (int kt = 0; kt < NT; ++kt) rounds[kt] = 0;
+      Ring qr;
+      for (int s = s_lo; ok && s < s_hi; ++s) {
+        const int n = ks_entries<MODE>(p, s);
+        const int t0 = first_tile(0, n), T = nt - t0;
+        if (MODE == SCAN_SCORES && T == 0) continue;
+        int mine[NT];
+#pragma unroll
+        for (int kt = 0; kt < NT; ++kt) mine[kt] = first_tile(kt, n) - t0;
+        const int list = list_of_slice(s);
+        if (list != loaded) {
+          loaded = list;
+          ok = ks_poll(key_full, loads & 1, abort_flag, wait_ns);
+          ++loads;
+          fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
+        }
+        for (int t = 0; ok && t < T; ++t) {
+#pragma unroll
+          for (int m = 0; m < NK; ++m) {
+            const int st = qr.st;
+            ok = ok && ks_poll(q_full + st, qr.ph, abort_flag, wait_ns);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT), q = sdesc_at(dQ, st * Sh::QST);
+            qr.next(NST);
+            const uint64_t q = sdesc_at(dQ, st * Sh::QST);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              mma_ss(tbase + (kt * 2 + b) * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
-                     sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
-            if (m == NK - 1) tc_commit(s_full + kt * 2 + b);
+            for (int kt = 0; kt < NT; ++kt) {
+              if (t < mine[kt] || !ok) continue;
+              const int b = rounds[kt] % NB;
+              if (m == 0) ok = ks_poll(s_empty + kt * NB + b, ((rounds[kt] / NB) & 1) ^ 1, abort_flag, wait_ns);
+              if (!ok) continue;
+              tc_fence_after();
+              const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+                mma_ss(tbase + (kt * NB + b) * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
+                       sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
+              if (m == NK - 1) {
+                tc_commit(s_full + kt * NB + b);
+                ++rounds[kt];
+              }
+            }
+            if (!ok) break;
+            tc_commit(q_empty + st);
           }
-          if (!ok) break;
-          tc_commit(q_empty + st);
         }
       }
       tc_commit(drain);
@@ -939,6 +1053,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     }
   } else if (MODE == SCAN_WEIGHTS) {
     // ------------------------------------------------------------ queries by TMA
+    const int s = s_lo, n = ks_entries<MODE>(p, s), PT = pl.PT;
+    const int t0 = first_tile(0, n), T = nt - t0;
     unsigned pend = 0, par = 0;
     auto lse_of = [&](int t, int v) {   // log2-unit lse of column v of query tile t; +inf: adds nothing
       const int i = (t0 + t) * PT + v / p.G;
@@ -953,7 +1069,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
       const int st = t % NST, u2 = t / NST, sl = t % NL;
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty + st, (u2 & 1) ^ 1, abort_flag, wait_ns))) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full + st, (uint32_t)KT * q_box * p.G * 128u);
+        mbar_arrive_expect_tx(q_full + st, (uint32_t)KT * pl.q_box * p.G * 128u);
 #pragma unroll
         for (int a = 0; a < KT; ++a)
           tma_load_3d(sm + Sh::OFF_Q + st * Sh::QST + a * N * 128, &tq, a * 64, g * p.G, s * p.Nq + (t0 + t) * PT, q_full + st);
@@ -985,9 +1101,9 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     constexpr int CPR = D / 8, STEP = Sh::NQW * 32, NX = N * CPR / STEP;
     const int qt = tid - Sh::W_Q * 32;
     const uint16_t* qg = static_cast<const uint16_t*>(p.q);
-    // this thread's 16-byte words of query tile t, one tile ahead
+    // this thread's 16-byte words of a query tile
     uint4 x[NX];
-    auto fetch = [&](int t) {
+    auto fetch = [&](int s, int t) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
         const int f = i * STEP + qt, v = t * N + f / CPR;
@@ -997,24 +1113,28 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
         x[i] = v < p.NV ? y : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    fetch(0);
     bool ok = true;
-    int kk = 0;
-    for (int t = 0; ok && t < T; ++t) {
+    Ring qr;
+    for (int s = s_lo; ok && s < s_hi; ++s) {
+      if (first_tile(0, ks_entries<MODE>(p, s)) == nt) continue;
+      fetch(s, 0);
+      for (int t = 0; ok && t < nt; ++t) {
 #pragma unroll
-      for (int m = 0; m < NK; ++m, ++kk) {
-        const int st = kk % NST;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, ((kk / NST) & 1) ^ 1, abort_flag, wait_ns)))) break;
-        unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
+        for (int m = 0; m < NK; ++m) {
+          const int st = qr.st;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, qr.ph ^ 1u, abort_flag, wait_ns)))) break;
+          qr.next(NST);
+          unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-          const int f = i * STEP + qt, r = f / CPR, c = f % CPR;
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x[i], m == 0, bf16);
+          for (int i = 0; i < NX; ++i) {
+            const int f = i * STEP + qt, r = f / CPR, c = f % CPR;
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x[i], m == 0, bf16);
+          }
+          if (m == NK - 1 && t + 1 < nt) fetch(s, t + 1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full + st);
         }
-        if (m == NK - 1 && t + 1 < T) fetch(t + 1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full + st);
       }
     }
   }
@@ -1080,20 +1200,41 @@ cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   memset(&tq, 0, sizeof(tq));
-  int PT = 0, q_box = 0;
+  PromptPlan pl;
+  memset(&pl, 0, sizeof(pl));
+  pl.sc = 1;
+  const int tiles = (p.L + ks::BM - 1) / ks::BM;
+  const long long slots = (long long)ks_sms() * Sh::CTAS;
   if (MODE == SCAN_WEIGHTS) {
-    PT = Sh::N / p.G;
+    pl.PT = Sh::N / p.G;
     const long long queries = (long long)p.S * p.Nq;
-    q_box = (int)(queries < PT ? queries : PT);
+    pl.q_box = (int)(queries < pl.PT ? queries : pl.PT);
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)queries};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * p.Hq * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)q_box};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)pl.q_box};
     if (!tmap_encode_3d(&tq, p.q_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.q, dims,
                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
+    // Batches of at most NT key tiles per (slice, KV head): as many as fill
+    // the rounds of CTAs that full batches would take, so that the last round
+    // is a full one of slightly smaller batches (16,384 keys of 8 heads: 38
+    // batches of 3 or 4 tiles in two rounds, not 32 of 4 in 1.7).
+    const long long units = (long long)p.S * p.Hkv;
+    const int full = (tiles + Sh::NT - 1) / Sh::NT;
+    const long long rounds = (units * full + slots - 1) / slots;
+    const long long nb = rounds * slots / units;
+    pl.nb = (int)(nb < full ? full : nb > tiles ? tiles : nb);
+  } else {
+    // Slices that share a sequence share its staged bounds: as many of them
+    // per CTA as leave a CTA for every slot
+    pl.nb = tiles;
+    const long long units = (long long)p.Hkv * tiles;
+    while (pl.sc < 8 && units * ((p.S + 2 * pl.sc - 1) / (2 * pl.sc)) >= slots) pl.sc *= 2;
   }
-  const int keys = Sh::NT * ks::BM;
-  kern<<<dim3((p.L + keys - 1) / keys, p.Hkv, p.S), Sh::THREADS, Sh::SMEM, st>>>(p, PT, q_box, tq);
+  pl.chunks = (p.S + pl.sc - 1) / pl.sc;
+  const long long grid = (long long)pl.nb * p.Hkv * pl.chunks;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kern<<<(unsigned)grid, Sh::THREADS, Sh::SMEM, st>>>(p, pl, tq);
   return cudaGetLastError();
 }
 
@@ -1111,8 +1252,8 @@ cudaError_t ks_weights_kind(const KeyScanParams& p, int D, cudaStream_t st) {
 
 }  // namespace
 
-// G <= 64: a query tile of the prompt form holds whole queries.
-bool keyscan_supported(int D, int G) { return (D == 64 || D == 128 || D == 256) && G <= 64; }
+// A query tile of the prompt form holds whole queries (64 vectors at D 256, else 128).
+bool keyscan_supported(int D, int G) { return (D == 64 || D == 128 || D == 256) && G <= (D == 256 ? 64 : 128); }
 
 cudaError_t keyscan_weights(const KeyScanParams& p, int D, int kind, cudaStream_t st) {
   switch (kind) {
