@@ -131,6 +131,9 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kMaxGrid = 65535;   // blocks in the y and z dimensions of a launch
 
+// More 128-entry tiles over all lists than the key-scan kernels count.
+bool too_many_tiles(int S, int Hkv, int L) { return (long long)S * Hkv * (((long long)L + 127) / 128) > 0x7fffffffLL; }
+
 struct Span {
   const void* p;
   size_t n;
@@ -642,6 +645,8 @@ fa_status fa_rows_weights(const fa_rows_args* a, const float* lse, float decay, 
   if (c.D > 256 || far::kv_row_bytes(kind, c.D) % 16 != 0)
     return fail(FA_ERR_UNSUPPORTED, "weights need D <= 256 and 16-byte multiples per (row, KV head); got D=%d", c.D);
   if (c.S > kMaxGrid || c.Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices and KV heads", kMaxGrid);
+  if (too_many_tiles(c.S, c.Hkv, c.list_len) || (long long)c.Nq * c.Hq > (1 << 30))
+    return fail(FA_ERR_UNSUPPORTED, "S * Hkv * L / 128 must fit int32, and Nq * Hq 2^30");
   if ((long long)c.S * c.Nq == 0 || c.list_len == 0) return FA_OK;
   if (!lse || !aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be the fp32 [S, Nq, Hq] of the attention call");
   if (!isfinite(decay)) return fail(FA_ERR_INVALID_ARG, "decay must be finite");
@@ -778,6 +783,8 @@ fa_status fa_kv_block_scores(const void* q, fa_dtype q_dtype, int32_t S, int32_t
   if (S > kMaxGrid || Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices and KV heads", kMaxGrid);
   if (!slice_seq && S > n_seq) return fail(FA_ERR_INVALID_ARG, "%d slices need as many page-table rows (got %d)", S, n_seq);
   if ((long long)max_pages * far::kPage > 0x7fffffffLL) return fail(FA_ERR_INVALID_ARG, "max_pages*64 overflows int32");
+  if (too_many_tiles(S, Hkv, max_pages) || (long long)Nq * Hq > (1 << 30))
+    return fail(FA_ERR_UNSUPPORTED, "S * Hkv * max_pages / 128 must fit int32, and Nq * Hq 2^30");
   if ((long long)S * Nq == 0 || max_pages == 0) return FA_OK;
   if (!q || !kmin || !kmax || !page_table || !seq_len || !score) return fail(FA_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(q, 16) || !aligned(kmin, 16) || !aligned(kmax, 16) || !aligned(page_table, 4) || !aligned(seq_len, 4) ||

@@ -12,15 +12,18 @@
 // One CTA per SM walks an even share of all (slice, KV head, tile) triples,
 // whatever the slices' lengths: every CTA adds up the tile counts itself and
 // finds its first triple (list lengths are on the device).  Warps:
-//   0-3    reduction: thread t owns key t of the tile; tensor-memory loads of
-//          its row, the reduction, the update of the output
-//   4      MMA issue (one lane); allocates tensor memory
-//   5      queries of the next (slice, KV head), into one of two buffers: its
+//   0-7    reduction: two warpgroups on alternate tiles; thread t owns key t of
+//          the tile: tensor-memory loads of its row, the reduction, the update
+//          of the output
+//   8      MMA issue; allocates tensor memory
+//   9      queries of the next (slice, KV head), into one of two buffers: its
 //          rows and, for weights, lse in log2 units and the causal limits
-//   6-13   keys: four warps for each 64-row half of a tile; cp.async of the
-//          listed rows into the 128-byte-swizzled layout, or one TMA tile load
-//          per 64 columns where the half is one contiguous pool run.  The
-//          copies arrive on the stage's barrier by themselves.
+//   10-17  keys: two groups of four warps on alternate tiles (one group's
+//          instructions per tile take longer than the tile's share of HBM
+//          time), two warps for each 64-row half; cp.async of the listed rows
+//          into the 128-byte-swizzled layout, or one TMA tile load per 64
+//          columns where the half is one contiguous pool run.  The copies
+//          arrive on the stage's barrier by themselves.
 // Scores take two stages per tile (kmax with max(q, 0), then kmin with
 // min(q, 0)), accumulated by the tensor core.  Codes of quantised pools are
 // copied to a ring in shared memory, widened exactly to Q's type by the lanes
@@ -40,12 +43,20 @@ namespace far {
 
 namespace ks {
 constexpr int BM = 128;                    // keys per tile
-constexpr int NEPI = 4, W_MMA = 4, W_Q = 5, W_KEY = 6, NKEY = 8;
+constexpr int NEPI = 8, W_MMA = 8, W_Q = 9, W_KEY = 10, NKEY = 8;
+constexpr int NBUF = 4;                    // accumulators
 constexpr int NWARP = W_KEY + NKEY;
 constexpr int THREADS = NWARP * 32;
 constexpr int MAXST = 8;
 constexpr int MAXN = kScanStreamVec;
-constexpr int PRE = 6;                     // tiles ahead that list entries are loaded
+constexpr int PRE = 3;                     // own tiles ahead that a key warp loads list entries
+// Groups of key warps on alternate tiles: two, but one for the codes of D 256
+// (two groups' code rings do not fit beside their operand stage) and for its
+// scores (two or fewer stages).  A stage's barrier tells two neighbouring
+// phases apart, so with two groups there must be more stages than a tile uses:
+// then whoever waits for a stage's last use knows that the use before it is over.
+template <int D, int NK, bool QUANT>
+constexpr int kGroups = D > 128 && (QUANT || NK == 2) ? 1 : 2;
 constexpr int SMEM_MAX = 225 * 1024;
 }  // namespace ks
 
@@ -53,11 +64,12 @@ namespace {
 
 enum { SCAN_WEIGHTS = 0, SCAN_SCORES = 1 };
 
-// Tiles of codes in flight beside the one being widened: as many as the
-// shared memory beside 64 query vectors and the operand stages holds, at most PRE.
+// Tiles of codes that a group of key warps has in flight beside the one it
+// widens: as many as the shared memory beside 64 query vectors and the operand
+// stages holds, at most PRE.
 template <int D, int KIND>
 __host__ __device__ constexpr int ks_ahead() {
-  const int code = ks::BM * kv_row_bytes<KIND>(D);
+  const int code = ks::kGroups<D, 1, true> * ks::BM * kv_row_bytes<KIND>(D);
   const int room = ks::SMEM_MAX - 3072 - 2 * ks::MAXN * D * 2 - (D <= 128 ? 2 : 1) * ks::BM * D * 2;
   const int n = room / code - 1;
   return n > ks::PRE ? ks::PRE : n;
@@ -84,7 +96,7 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   if (QUANT) {
     // two operand stages (one for D 256), the code ring
     l.nst = D <= 128 ? 2 : 1;
-    l.ncs = ks_ahead<D, KIND>() + 1;
+    l.ncs = ks::kGroups<D, 1, true> * (ks_ahead<D, KIND>() + 1);
   } else {
     l.nst = room / l.tile;
     l.nst = l.nst > ks::MAXST ? ks::MAXST : l.nst;
@@ -92,7 +104,7 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   }
   l.off_c = l.off_k + l.nst * l.tile;
   l.off_bar = l.off_c + l.ncs * l.code;
-  l.off_misc = l.off_bar + (2 * ks::MAXST + 4 + 4 + 1) * 8;
+  l.off_misc = l.off_bar + (2 * ks::MAXST + 2 * ks::NBUF + 4 + 1) * 8;
   l.off_l = (l.off_misc + 32 + 15) / 16 * 16;
   l.total = l.off_l + 2 * ks::MAXN * 8 + 1024;
   return l;
@@ -162,18 +174,54 @@ __device__ __forceinline__ void ks_wait_drain(uint64_t* b, uint32_t parity) {
   }
 }
 
-// The MMA lane's wait: polls, so that the time limit holds to the poll.
+// The MMA warp's wait: polls, so that the time limit holds to the poll.  The
+// warp stays converged, and one elected lane issues: descriptors of a
+// converged warp are kept in uniform registers.
 __device__ __forceinline__ bool ks_poll(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
-  if (mbar_test_wait(b, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_test_wait(b, parity))) return true;
   const unsigned long long t0 = globaltimer();
-  while (!mbar_test_wait(b, parity)) {
-    if (*abort) return false;
-    if (globaltimer() - t0 > limit_ns) {
+  while (!__all_sync(0xffffffffu, mbar_test_wait(b, parity))) {
+    const bool late = globaltimer() - t0 > limit_ns;
+    if (__any_sync(0xffffffffu, late || *abort)) {
       *abort = 1;
       return false;
     }
   }
   return true;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(x));
+  return x != 0;
+}
+
+// sum + 2^x, two at a time, on the FMA pipe: the exponential unit gives 16
+// results a clock and SM, the FMA pipe 128 operations.  x = n + f with n the
+// nearest integer (added to and taken back from 1.5 * 2^23, whose low bits
+// then hold it; 127 more makes them 2^n's exponent field), 2^f on [-1/2, 1/2]
+// by a degree-5 polynomial, the least-maximum fit of the relative error
+// (7.5e-8; 2.0e-7 evaluated in fp32).  x is clamped to [-126, 128]: below, 2^x
+// counts as 2^-126; from 128 on the exponent field is infinity's.  A NaN goes through f.
+__device__ __forceinline__ float2 exp2_poly_add(float2 x, float2 sum) {
+  auto clamp = [](float v) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(y) : "f"(v));
+    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(y));
+    return y;
+  };
+  x = make_float2(clamp(x.x), clamp(x.y));
+  const float M = 12583039.0f;   // 1.5 * 2^23 + 127
+  const float2 t = __fadd2_rn(x, make_float2(M, M));
+  const float2 r = __fadd2_rn(t, make_float2(-M, -M));
+  const float2 f = __fadd2_rn(x, make_float2(-r.x, -r.y));
+  auto c = [](float v) { return make_float2(v, v); };
+  float2 q = __ffma2_rn(f, c(0.0013276472f), c(0.0096755414f));
+  q = __ffma2_rn(q, f, c(0.055507133f));
+  q = __ffma2_rn(q, f, c(0.2402212f));
+  q = __ffma2_rn(q, f, c(0.69314697f));
+  q = __ffma2_rn(q, f, c(1.0000001f));
+  const float2 e = make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23));
+  return __ffma2_rn(q, e, sum);
 }
 
 // 16 bytes of pool codes -> 16-bit values of Q's type, as 16-byte words.
@@ -234,84 +282,106 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const KsLayout ly = ks_layout<D, MODE, KIND>(p.NV);
-  const int N = ly.N, NST = ly.nst;
+  const int N = ly.N, NST = ly.nst;   // two groups of key warps: NST > NK (see kGroups)
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + ly.off_bar);
   uint64_t* k_empty = k_full + MAXST;
   uint64_t* s_full = k_empty + MAXST;
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* q_full = s_empty + 2;
+  uint64_t* s_empty = s_full + NBUF;
+  uint64_t* q_full = s_empty + NBUF;
   uint64_t* q_empty = q_full + 2;
   uint64_t* drain = q_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + ly.off_misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + ly.off_misc + 4);
   float* l2 = reinterpret_cast<float*>(sm + ly.off_l);            // [2][MAXN] lse in log2 units
   int* lim = reinterpret_cast<int*>(sm + ly.off_l) + 2 * MAXN;    // [2][MAXN] n_s-relative causal limits
-  __shared__ long long scan_s[NWARP];
-  __shared__ int walk_s[3];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool bf16 = p.q_bf16 != 0;
   const unsigned long long wait_ns = p.wait_ns;
 
-  // ---- this CTA's share of the triples
-  long long total = 0;
+  // ---- this CTA's share of the triples: every warp adds up the slices' tile
+  // counts, 8 slices a lane and step, and finds the slice of its first tile
   Walk w0;
-  int mine = 0;   // tiles of this CTA's share
+  int mine;   // tiles of the share
   {
-    // tiles of all slices, THREADS slices at a time; then the slice that holds
-    // this CTA's first tile
-    for (int pass = 0; pass < 2; ++pass) {
-      long long carry = 0;
-      long long start = 0;
-      if (pass == 1) {
-        start = total * blockIdx.x / gridDim.x;
-        mine = (int)(total * (blockIdx.x + 1) / gridDim.x - start);
-        if (mine <= 0) return;
+    constexpr int PER = 8;
+    auto counts = [&](int base, int (&n)[PER], int (&c)[PER]) -> int {   // of 8 slices from base on; their sum
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) n[i] = base + i < p.S ? ks_entries<MODE>(p, base + i) : 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        c[i] = base + i < p.S ? ks_tiles<MODE>(n[i]) * p.Hkv : 0;
+        sum += c[i];
       }
-      for (int base = 0; base < p.S; base += THREADS) {
-        const int s = base + tid;
-        const int n = s < p.S ? ks_entries<MODE>(p, s) : 0;
-        const int T = s < p.S ? ks_tiles<MODE>(n) : 0;
-        const long long c = (long long)T * p.Hkv;
-        long long x = c;
+      return sum;
+    };
+    int n[PER], c[PER], total = 0;
+    if (MODE == SCAN_WEIGHTS && !p.len) {
+      total = ks_tiles<MODE>(p.L) * p.Hkv * p.S;
+    } else {
+      for (int base = 0; base < p.S; base += 32 * PER) total += __reduce_add_sync(0xffffffffu, counts(base + lane * PER, n, c));
+    }
+    // even shares, the first total % CTAs of them one tile longer
+    const int each = total / (int)gridDim.x, more = total % (int)gridDim.x, bid = (int)blockIdx.x;
+    const int start = bid * each + min(bid, more);
+    mine = each + (bid < more ? 1 : 0);
+    if (mine == 0) return;
+    int slice = 0, left = 0, len = p.L;   // the slice, and the share's start within it
+    if (MODE == SCAN_WEIGHTS && !p.len) {
+      const int per = ks_tiles<MODE>(p.L) * p.Hkv;
+      slice = start / per;
+      left = start % per;
+    } else {
+      int carry = 0;
+      for (int base = 0; base < p.S; base += 32 * PER) {
+        int x = counts(base + lane * PER, n, c);
+        const int sum = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
           if (lane >= o) x += y;
         }
-        if (lane == 31) scan_s[warp] = x;
-        __syncthreads();
-        long long before = carry, sum = 0;
-        for (int k = 0; k < NWARP; ++k) {
-          before += k < warp ? scan_s[k] : 0;
-          sum += scan_s[k];
+        const int before = carry + x - sum;
+        const unsigned who = __ballot_sync(0xffffffffu, start >= before && start < before + sum);
+        if (who) {
+          int at = before, found = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            if (!found && start < at + c[i]) {
+              found = 1;
+              slice = base + lane * PER + i;
+              left = start - at;
+              len = n[i];
+            }
+            at += c[i];
+          }
+          const int src = __ffs(who) - 1;
+          slice = __shfl_sync(0xffffffffu, slice, src);
+          left = __shfl_sync(0xffffffffu, left, src);
+          len = __shfl_sync(0xffffffffu, len, src);
+          break;
         }
-        before += x - c;
-        if (pass == 1 && start >= before && start < before + c) {
-          const long long r = start - before;
-          walk_s[0] = s;
-          walk_s[1] = (int)(r / T);
-          walk_s[2] = (int)(r % T);
-        }
-        carry += sum;
-        __syncthreads();
+        carry += __shfl_sync(0xffffffffu, x, 31);
       }
-      total = carry;
     }
-    w0.s = walk_s[0];
-    w0.g = walk_s[1];
-    w0.t = walk_s[2];
-    ks_enter<MODE>(p, w0);
+    w0.s = slice;
+    w0.n = len;
+    w0.T = ks_tiles<MODE>(len);
+    w0.g = left / w0.T;
+    w0.t = left % w0.T;
   }
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(k_full + i, QUANT ? NKEY : NKEY * 32);
+      mbar_init(k_full + i, NKEY / kGroups<D, NK, QUANT> * (QUANT ? 1 : 32));
       mbar_init(k_empty + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_empty + i, NEPI);
+      mbar_init(s_empty + i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1 + NEPI);   // the MMAs of its last tile, and the reduction warps
     }
@@ -320,7 +390,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
     mbar_fence_init();
   }
   uint32_t ncols = 32;
-  while ((int)ncols < 2 * N) ncols <<= 1;
+  while ((int)ncols < NBUF * N) ncols <<= 1;
   if (warp == W_MMA) {
     tmem_alloc(tmem_holder, ncols);
     tmem_relinquish();
@@ -332,7 +402,8 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 
   if (warp < NEPI) {
     // ------------------------------------------------------------ reduction
-    const uint32_t lanes = (uint32_t)warp << 21;   // tensor-memory lane base of this warp: 32 * warp, in bits 16 up
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // tensor-memory lane base of this warp: 32 * (warp % 4), in bits 16 up
+    const int grp = warp >> 2, kid = tid & 127;          // this warpgroup's tiles: grp, grp + 2, ...
     // What a thread needs of its key beside the products: loaded one tile
     // ahead into one of two register sets, which the loop names in turn (a
     // copy from one to the other would wait for the load).
@@ -342,7 +413,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       float old;
     };
     auto load_key = [&](const Walk& x, Key& a) {
-      const int j = x.t * BM + tid;
+      const int j = x.t * BM + kid;
       a.row = -1;
       a.old = 0.f;
       if (j < x.n) {
@@ -356,21 +427,42 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       if (QUANT) a.scale = live(a) ? __ldg(p.k_scale + ((size_t)(a.row >> 6) * p.Hkv + x.g) * kPage + (a.row & 63)) : (unsigned short)0;
     };
     Walk w = w0;
-    int unit = 0;
-    // one tile: its key in cur; the next tile's goes to nxt
+    int unit = 0, unit_seen = -1;
+    // The queries of the current (slice, KV head) are in their buffer.
+    auto have_queries = [&]() {
+      if (unit == unit_seen) return true;
+      unit_seen = unit;
+      return (bool)__all_sync(0xffffffffu, mbar_wait(q_full + (unit & 1), (unit >> 1) & 1, abort_flag, wait_ns));
+    };
+    // Over one tile of the share, whichever warpgroup's; the next (slice, KV
+    // head) begins after its last.  Both warpgroups count the query buffers so, and
+    // each gives a buffer back when it has passed the last tile that uses it:
+    // after seeing it full, since an arrival any earlier could fall into the
+    // phase of the buffer's use before.
+    auto pass = [&](int k, Walk& x) -> bool {
+      const bool last = k + 1 == mine || x.t + 1 == x.T;
+      if (last) {
+        if (!have_queries()) return false;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + (unit & 1));
+        ++unit;
+      }
+      if (k + 1 < mine) ks_next<MODE>(p, x);
+      return true;
+    };
+    // one tile: its key in cur; the group's next tile's goes to nxt
     auto tile = [&](int k, Key& cur, Key& nxt) -> bool {
-      const int b = k & 1, qb = unit & 1;
-      const bool first = k == 0 || w.t == 0;
-      const bool last = k + 1 == mine || w.t + 1 == w.T;
-      const int j = w.t * BM + tid;
+      const int b = k % NBUF, qb = unit & 1;
+      const int j = w.t * BM + kid;
       float* out = p.out + ((size_t)w.s * p.Hkv + w.g) * p.L;
       Walk nx = w;
-      if (k + 1 < mine) {
+      if (k + 2 < mine) {
+        ks_next<MODE>(p, nx);
         ks_next<MODE>(p, nx);
         load_key(nx, nxt);
       }
-      if (first && !__all_sync(0xffffffffu, mbar_wait(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns))) return false;
-      if (!__all_sync(0xffffffffu, mbar_wait(s_full + b, (k >> 1) & 1, abort_flag, wait_ns))) return false;
+      if (!have_queries()) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full + b, (k / NBUF) & 1, abort_flag, wait_ns))) return false;
       tc_fence_after();
       const float4* l4 = reinterpret_cast<const float4*>(l2 + qb * MAXN);
       const int4* m4 = reinterpret_cast<const int4*>(lim + qb * MAXN);
@@ -394,97 +486,103 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
           // l = +inf and add nothing whatever their product.  Selections, not
           // branches: a branch per column made this loop the kernel's bound
           // (45.7 us where selections take 31, 4 x 16,384 entries).
+          float e[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 l = l4[c0 / 4 + i];
             const float lv[4] = {l.x, l.y, l.z, l.w};
-            float e[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              e[u] = fast_ex2(fmaf(__uint_as_float(x[4 * i + u]), cs, -lv[u]));
-              e[u] = lv[u] == INF ? 0.f : e[u];
+              const float ex = fast_ex2(fmaf(__uint_as_float(x[4 * i + u]), cs, -lv[u]));
+              e[4 * i + u] = lv[u] == INF ? 0.f : ex;
             }
-            if (masked) {
-              const int4 m = m4[c0 / 4 + i];
-              e[0] = j <= m.x ? e[0] : 0.f;
-              e[1] = j <= m.y ? e[1] : 0.f;
-              e[2] = j <= m.z ? e[2] : 0.f;
-              e[3] = j <= m.w ? e[3] : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) r[u] += e[u];
           }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int4 m = m4[c0 / 4 + i];
+              e[4 * i] = j <= m.x ? e[4 * i] : 0.f;
+              e[4 * i + 1] = j <= m.y ? e[4 * i + 1] : 0.f;
+              e[4 * i + 2] = j <= m.z ? e[4 * i + 2] : 0.f;
+              e[4 * i + 3] = j <= m.w ? e[4 * i + 3] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i & 3] += e[i];
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(s_empty + b);
-        if (last) mbar_arrive(q_empty + qb);
-      }
+      if (lane == 0) mbar_arrive(s_empty + b);
       if (MODE == SCAN_SCORES) {
         if (j < w.n) out[j] = live(cur) ? max_nan2(max_nan2(r[0], r[1]), max_nan2(r[2], r[3])) : -INF;
         // past the sequence's blocks: the (slice, KV head)'s last tile fills the rest
         if (w.t + 1 == w.T)
-          for (int f = w.n + tid; f < p.L; f += NEPI * 32) out[f] = -INF;
+          for (int f = w.n + kid; f < p.L; f += 128) out[f] = -INF;
       } else if (j < w.n) {
         const float add = live(cur) ? (r[0] + r[1]) + (r[2] + r[3]) : 0.f;
         out[j] = p.decay == 0.f ? add : fmaf(p.decay, cur.old, add);
       }
-      if (k + 1 < mine) load_scale(nx, nxt);
-      if (last) ++unit;
-      w = nx;
-      return true;
+      if (k + 2 < mine) load_scale(nx, nxt);
+      return pass(k, w) && (k + 1 >= mine || pass(k + 1, w));
     };
     Key ka, kb;
-    load_key(w, ka);
-    load_scale(w, ka);
-    for (int k = 0; k < mine; k += 2) {
+    const bool begun = grp == 0 || pass(0, w);
+    if (begun && grp < mine) {
+      load_key(w, ka);
+      load_scale(w, ka);
+    }
+    for (int k = grp; begun && k < mine; k += 4) {
       if (!tile(k, ka, kb)) break;
-      if (k + 1 < mine && !tile(k + 1, kb, ka)) break;
+      if (k + 2 < mine && !tile(k + 2, kb, ka)) break;
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const uint32_t id = make_idesc_f16(BM, N, bf16, false);
-      const uint64_t dK = sdesc_sw128(smem_u32(sm + ly.off_k), 16, 1024);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sm + ly.off_q), 16, 1024);
-      const uint32_t qatom = (uint32_t)N * 128;
-      Walk w = w0;
-      int unit = 0;
-      bool ok = true;
-      Ring kr;
-      for (int k = 0; ok && k < mine; ++k) {
-        const int b = k & 1, qb = unit & 1;
-        const bool first = k == 0 || w.t == 0, last = k + 1 == mine || w.t + 1 == w.T;
-        if (first) ok = ks_poll(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns);
-        ok = ok && ks_poll(s_empty + b, ((k >> 1) & 1) ^ 1, abort_flag, wait_ns);
+    const uint32_t id = make_idesc_f16(BM, N, bf16, false);
+    const uint64_t dK = sdesc_sw128(smem_u32(sm + ly.off_k), 16, 1024);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sm + ly.off_q), 16, 1024);
+    const uint32_t qatom = (uint32_t)N * 128;
+    Walk w = w0;
+    int unit = 0;
+    bool ok = true;
+    Ring kr, sr;
+    for (int k = 0; ok && k < mine; ++k) {
+      const int qb = unit & 1;
+      const bool first = k == 0 || w.t == 0, last = k + 1 == mine || w.t + 1 == w.T;
+      if (first) ok = ks_poll(q_full + qb, (unit >> 1) & 1, abort_flag, wait_ns);
+      ok = ok && ks_poll(s_empty + sr.st, sr.ph ^ 1u, abort_flag, wait_ns);
 #pragma unroll
-        for (int m = 0; m < NK; ++m) {
-          const int st = kr.st;
-          ok = ok && ks_poll(k_full + st, kr.ph, abort_flag, wait_ns);
-          if (!ok) break;
-          kr.next(NST);
-          tc_fence_after();
+      for (int m = 0; m < NK; ++m) {
+        const int st = kr.st;
+        ok = ok && ks_poll(k_full + st, kr.ph, abort_flag, wait_ns);
+        if (!ok) break;
+        kr.next(NST);
+        tc_fence_after();
+        const uint64_t a = sdesc_at(dK, st * ly.tile), q = sdesc_at(dQ, qb * ly.qb_bytes + m * KT * qatom);
+        if (elect_one()) {
           fence_proxy_async_smem();   // the stage's cp.async copies arrived by themselves
-          const uint64_t a = sdesc_at(dK, st * ly.tile), q = sdesc_at(dQ, qb * ly.qb_bytes + m * KT * qatom);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
-            mma_ss(tbase + b * N, sdesc_at(a, (i >> 2) * ATOM + (i & 3) * 32), sdesc_at(q, (i >> 2) * qatom + (i & 3) * 32),
+            mma_ss(tbase + sr.st * N, sdesc_at(a, (i >> 2) * ATOM + (i & 3) * 32), sdesc_at(q, (i >> 2) * qatom + (i & 3) * 32),
                    id, m > 0 || i > 0);
           tc_commit(k_empty + st);
+          if (m == NK - 1) {
+            tc_commit(s_full + sr.st);
+            if (last) tc_commit(q_empty + qb);
+          }
         }
-        if (!ok) break;
-        tc_commit(s_full + b);
-        if (last) {
-          tc_commit(q_empty + qb);
-          ++unit;
-        }
-        if (k + 1 < mine) ks_next<MODE>(p, w);
+        __syncwarp();
       }
+      if (!ok) break;
+      sr.next(NBUF);
+      if (last) ++unit;
+      if (k + 1 < mine) ks_next<MODE>(p, w);
+    }
+    if (elect_one()) {
       tc_commit(drain);
       ks_wait_drain(drain, 0);
     }
+    __syncwarp();
   } else if (warp == W_Q) {
     // ------------------------------------------------------------ queries
     Walk w = w0;
@@ -529,9 +627,25 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ keys
-    const int kw = warp - W_KEY;
-    const int half = kw >> 2, quarter = kw & 3;   // 64-row half of the tile, 16 rows of it
+    constexpr int GROUPS = kGroups<D, NK, QUANT>, GW = NKEY / GROUPS, RW = BM / GW;   // warps of a group, rows of a warp
+    const int grp = (warp - W_KEY) / GW, kw = (warp - W_KEY) % GW;
+    // this group's tiles: grp, grp + GROUPS, ...; n_own of them
+    const int n_own = (mine - grp + GROUPS - 1) / GROUPS;
+    auto step = [&](Walk& x) {   // to the group's next tile (there is one)
+#pragma unroll
+      for (int i = 0; i < GROUPS; ++i) ks_next<MODE>(p, x);
+    };
     Walk w = w0;
+    Ring kr;
+    if (grp == 1 && n_own > 0) {
+      ks_next<MODE>(p, w);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) kr.next(NST);
+    }
+    auto advance = [&]() {       // over the other group's stages
+#pragma unroll
+      for (int i = 0; i < (GROUPS - 1) * NK; ++i) kr.next(NST);
+    };
     auto list_of_slice = [&](const Walk& x) {
       return MODE == SCAN_SCORES && p.slice_seq ? (size_t)max(__ldg(p.slice_seq + x.s), 0) : (size_t)x.s;
     };
@@ -543,6 +657,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
     if constexpr (!QUANT) {
       constexpr int CPR = D / 8;
       unsigned tma_pend = 0, tma_par = 0;
+      const int half = kw / (GW / 2), sub = kw % (GW / 2);   // 64-row half of the tile, RW rows of it
       // List entries PRE tiles ahead (a tile's share of HBM time is shorter
       // than the latency of a list load), in register sets that the unrolled
       // loop names in turn.
@@ -550,30 +665,30 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       Walk wp = w;
       int kp = 0;
       auto fetch = [&](int& a, int& b) {
-        if (kp < mine) {
+        if (kp < n_own) {
           a = entry(wp, half * 64 + lane);
           b = entry(wp, half * 64 + 32 + lane);
-          if (++kp < mine) ks_next<MODE>(p, wp);
+          if (++kp < n_own) step(wp);
         }
       };
 #pragma unroll
       for (int i = 0; i < PRE; ++i) fetch(nx0[i], nx1[i]);
-      Ring kr;
       bool ok = true;
-      for (int k0 = 0; ok && k0 < mine; k0 += PRE) {
+      for (int k0 = 0; ok && k0 < n_own; k0 += PRE) {
 #pragma unroll
         for (int i = 0; i < PRE; ++i) {
-          if (!ok || k0 + i >= mine) break;
+          if (!ok || k0 + i >= n_own) break;
           const int r0 = row_of(nx0[i]), r1 = row_of(nx1[i]), g = w.g;
           const int base = __shfl_sync(0xffffffffu, r0, 0);
           const bool run = __all_sync(0xffffffffu, r0 >= 0 && r0 == base + lane && r1 == base + 32 + lane) && tma_ok;
+          const int own = sub * RW < 32 ? r0 : r1;   // the register that holds this warp's rows
 #pragma unroll
           for (int m = 0; m < NK; ++m) {
             const int st = kr.st;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, kr.ph ^ 1u, abort_flag, wait_ns)))) break;
             unsigned char* dst = sm + ly.off_k + st * ly.tile + half * 64 * 128;
             if (run) {
-              if (quarter == 0 && lane == 0) {
+              if (sub == 0 && lane == 0) {
                 mbar_arrive_expect_tx(k_full + st, 64 * D * 2);
 #pragma unroll
                 for (int a = 0; a < KT; ++a) tma_load_3d(dst + a * ATOM, m ? &t1 : &t0, a * 64, g, base, k_full + st);
@@ -585,49 +700,50 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
             } else {
               const char* src = static_cast<const char*>(p.k[m]) + (size_t)g * (D * 2);
               const size_t pitch = (size_t)p.Hkv * (D * 2);
+              unsigned char* mine_dst = dst + sub * RW * 128;
 #pragma unroll
-              for (int it = 0; it < 16 * CPR / 32; ++it) {
+              for (int it = 0; it < RW * CPR / 32; ++it) {
                 const int f = it * 32 + lane;
-                const int e = quarter * 16 + f / CPR, c = f % CPR;   // row of the half, chunk
-                // a quarter's 16 rows lie in one of the two registers
-                const int r = __shfl_sync(0xffffffffu, quarter < 2 ? r0 : r1, e & 31);
-                cp_async16(dst + (c >> 3) * ATOM + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + (r >= 0 ? r : 0) * pitch + c * 16,
+                const int e = f / CPR, c = f % CPR;   // row of the warp's RW, chunk
+                const int r = __shfl_sync(0xffffffffu, own, (sub * RW + e) & 31);
+                cp_async16(mine_dst + (c >> 3) * ATOM + e * 128 + (((c & 7) ^ (e & 7)) << 4), src + (r >= 0 ? r : 0) * pitch + c * 16,
                            r >= 0);
               }
               cp_async_mbar_arrive_noinc(k_full + st);
             }
             kr.next(NST);
           }
+          advance();
           fetch(nx0[i], nx1[i]);
-          if (k0 + i + 1 < mine) ks_next<MODE>(p, w);
+          if (k0 + i + 1 < n_own) step(w);
         }
       }
       cp_async_wait_all();
-      if (*abort_flag && quarter == 0 && lane == 0) {   // no TMA load may still be writing when the CTA exits
+      if (*abort_flag && sub == 0 && lane == 0) {   // no TMA load may still be writing when the CTA exits
         for (int i = 0; i < NST; ++i)
           if ((tma_pend >> i) & 1u) ks_wait_drain(k_full + i, (tma_par >> i) & 1u);
       }
     } else {
-      // 16 rows of every tile per warp; each lane copies, and later widens, its
-      // own 16-byte chunks, which lie lane by lane in the code ring
-      constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, NIT = 16 * CPR / 32;
-      static_assert(16 * CPR % 32 == 0, "a warp's chunks fill its lanes");
+      // RW rows of each of the group's tiles per warp; each lane copies, and
+      // later widens, its own 16-byte chunks, which lie lane by lane in the code ring
+      constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, NIT = RW * CPR / 32;
+      static_assert(RW * CPR % 32 == 0, "a warp's chunks fill its lanes");
       constexpr int AHEAD = ks_ahead<D, KIND>(), NCS = AHEAD + 1;
-      unsigned char* ring = sm + ly.off_c + kw * 16 * CB;
+      unsigned char* ring = sm + ly.off_c + grp * NCS * ly.code + kw * RW * CB;
       Walk wi = w, wp = w;                          // the copies' walk, NCS tiles ahead; the list entries', PRE more
-      int nx[PRE];                                  // rows of the next tiles to copy, lanes 0-15
+      int nx[PRE];                                  // rows of the next tiles to copy, lanes 0 .. RW - 1
       int ki = 0, kp = 0, slot = 0;
       auto fetch = [&](int& a) {
-        if (kp < mine) {
-          a = entry(wp, kw * 16 + (lane & 15));
-          if (++kp < mine) ks_next<MODE>(p, wp);
+        if (kp < n_own) {
+          a = entry(wp, kw * RW + lane % RW);
+          if (++kp < n_own) step(wp);
         }
       };
 #pragma unroll
       for (int i = 0; i < PRE; ++i) fetch(nx[i]);
       // the copies of tile ki, whose list entries are in `set`; one group, empty past the share
       auto issue = [&](int& set) {
-        if (ki < mine) {
+        if (ki < n_own) {
           const int row = row_of(set), g = wi.g;
           unsigned char* dst = ring + slot * ly.code;
           if (++slot == NCS) slot = 0;
@@ -639,12 +755,11 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
             cp_async16(dst + f * 16, static_cast<const char*>(p.k[0]) + ((size_t)(okr ? r : 0) * p.Hkv + g) * CB + c * 16, okr);
           }
           fetch(set);
-          if (++ki < mine) ks_next<MODE>(p, wi);
+          if (++ki < n_own) step(wi);
         }
         cp_async_commit();
       };
       // one tile: widen it, issue the copies of the tile AHEAD later
-      Ring kr;
       int rd = 0;
       auto tile = [&](int& set) -> bool {
         // copies of this tile have landed once at most AHEAD - 1 later groups are pending
@@ -658,11 +773,12 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
         const int st = kr.st;
         if (!__all_sync(0xffffffffu, mbar_wait(k_empty + st, kr.ph ^ 1u, abort_flag, wait_ns))) return false;
         kr.next(NST);
+        advance();
         unsigned char* dst = sm + ly.off_k + st * ly.tile;
         constexpr int W = KvChunk<KIND>::N / 8;     // 16-byte words a chunk widens to
 #pragma unroll
         for (int it = 0; it < NIT; ++it) {
-          const int f = it * 32 + lane, e = kw * 16 + f / CPR, c = (f % CPR) * W;
+          const int f = it * 32 + lane, e = kw * RW + f / CPR, c = (f % CPR) * W;
           uint4 o[W];
           widen_chunk<KIND>(cw[it], bf16, o);
 #pragma unroll
@@ -678,10 +794,10 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) issue(nx[i]);
       bool ok = true;
-      for (int k0 = 0; ok && k0 < mine; k0 += PRE) {
+      for (int k0 = 0; ok && k0 < n_own; k0 += PRE) {
 #pragma unroll
         for (int i = 0; i < PRE; ++i) {
-          if (!ok || k0 + i >= mine) break;
+          if (!ok || k0 + i >= n_own) break;
           ok = tile(nx[(i + AHEAD) % PRE]);
         }
       }
@@ -703,16 +819,17 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 // Many query vectors (prompts): a CTA keeps its keys in shared memory and the
 // queries stream past them.
 //
-// Per 128 x 128 x 128 tile the tensor core takes 512 clocks and the
-// exponentials (32 a clock and SM) as many; a staged query tile, 256 rows of
-// 128 bytes to the TMA unit, takes about three times that.  So a CTA owns up to
-// NT = 4 tiles of 128 keys, each query tile is used for all of them, and one
-// warpgroup reduces each key tile (thread = key, as above) while the tensor core is at the
-// others.  The key tiles of a CTA are nb apart, so that under a causal limit
-// every CTA has early and late ones.
+// A CTA owns up to NT tiles of 128 keys, so that each staged query tile is
+// used NT times; one warpgroup reduces each key tile (thread = key, as above)
+// while the tensor core is at the others.  NBUF accumulators go round in the
+// order of the products, one more than there are key tiles: a key tile's next
+// product does not wait for the reduction of its last.  (More accumulators
+// than key tiles also keep a warpgroup's wait within one phase of its barrier:
+// the product before in the same accumulator is older than the
+// warpgroup's own last one.)
 // Scores (two stages per query tile, for max(q, 0) and min(q, 0)) keep both
-// bounds of one key tile and two CTAs per SM; a CTA walks several slices,
-// and stages the bounds again only where the slice is of another sequence.
+// bounds of one key tile; a CTA walks several slices, and stages the bounds
+// again only where the slice is of another sequence.
 //   warps 0 .. 4 NT - 1   gather (and widen) the keys, then the reduction
 //   then                  MMA issue; queries: TMA boxes of whole queries
 //                         (weights), or loads split by sign (scores)
@@ -720,13 +837,12 @@ namespace kp {
 template <int D, int MODE>
 struct Shape {
   static constexpr bool SC = MODE == SCAN_SCORES;
-  static constexpr int NT = SC ? 1 : D == 256 ? 2 : 4;      // key tiles
-  static constexpr int N = SC || D == 256 ? 64 : 128;       // query vectors per tile
-  static constexpr int NB = SC || D == 256 ? 2 : 1;         // accumulators per key tile
+  static constexpr int NT = SC ? 1 : D == 256 ? 2 : 3;      // key tiles
+  static constexpr int N = D == 256 ? 64 : 128;             // query vectors per tile
+  static constexpr int NBUF = 4;                            // accumulators
   static constexpr int NK = SC ? 2 : 1;                     // stages per query tile
-  static constexpr int NST = D == 64 ? 4 : 2;
+  static constexpr int NST = SC ? (D == 256 ? 2 : 4) : D == 64 ? 4 : D == 128 ? 3 : 2;
   static constexpr int NL = 4;                              // query tiles whose lse are on chip
-  static constexpr int CTAS = SC && D <= 128 ? 2 : 1;       // per SM
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
   static constexpr int QST = N * D * 2;               // one query stage
@@ -734,30 +850,30 @@ struct Shape {
   static constexpr int THREADS = (W_Q + NQW) * 32;
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
-  static constexpr int NBAR = 1 + 2 * NST + 2 * NB * NT + 1 + 2 * NL;
+  static constexpr int NBAR = 1 + 2 * NST + 2 * NBUF + 1 + 2 * NL;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NL][N] lse, [NL][N] limits, [NL] flags
   static constexpr int OFF_IDX = OFF_L + (SC ? 0 : NL * N * 8 + NL * 4);
   static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
   static constexpr int SMEM = USED + 1024;
-  static constexpr uint32_t COLS = NT * NB * N;
-  static_assert(COLS * CTAS <= 512 && (COLS & (COLS - 1)) == 0, "tensor memory");
-  static_assert((SMEM + 1024) * CTAS <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");
+  static constexpr uint32_t COLS = NBUF * N;
+  static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0, "tensor memory");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 }  // namespace kp
 
 struct PromptPlan {
   int PT, q_box;    // weights: queries per tile, and per TMA box
-  int nb;           // batches of key tiles per (slice, KV head); key tile kt of batch j is tile j + kt * nb
+  int nb, tiles;    // batches of key tiles per (slice, KV head), and key tiles of a list of L entries
   int sc, chunks;   // slices per CTA, chunks of slices
 };
 
 template <int D, int MODE, int KIND>
-__global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, MODE>::CTAS))
+__global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     keyscan_prompt_kernel(const KeyScanParams p, const PromptPlan pl, const __grid_constant__ CUtensorMap tq) {
   using Sh = kp::Shape<D, MODE>;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
-  constexpr int NT = Sh::NT, N = Sh::N, NB = Sh::NB, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
+  constexpr int NT = Sh::NT, N = Sh::N, NBUF = Sh::NBUF, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
   constexpr int BM = ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
@@ -765,15 +881,15 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
   uint64_t* key_full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t* q_full = key_full + 1;
   uint64_t* q_empty = q_full + NST;
-  uint64_t* s_full = q_empty + NST;      // [NT][NB]
-  uint64_t* s_empty = s_full + NB * NT;  // [NT][NB]
-  uint64_t* drain = s_empty + NB * NT;
+  uint64_t* s_full = q_empty + NST;
+  uint64_t* s_empty = s_full + NBUF;
+  uint64_t* drain = s_empty + NBUF;
   uint64_t* l_full = drain + 1;          // [NL] lse, limits and flag of a query tile
   uint64_t* l_empty = l_full + NL;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + Sh::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::OFF_MISC + 4);
-  float* l2 = reinterpret_cast<float*>(sm + Sh::OFF_L);
-  int* lim = reinterpret_cast<int*>(l2 + NL * N);
+  float* nl2 = reinterpret_cast<float*>(sm + Sh::OFF_L);   // minus lse, in log2 units; -inf adds nothing
+  int* lim = reinterpret_cast<int*>(nl2 + NL * N);
   int* odd = lim + NL * N;               // a column of the tile adds nothing, whatever its product
   int* idx = reinterpret_cast<int*>(sm + Sh::OFF_IDX);
 
@@ -785,16 +901,18 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
   const int batch = blockIdx.x / per, g = blockIdx.x % per % p.Hkv, chunk = blockIdx.x % per / p.Hkv;
   const int s_lo = chunk * pl.sc, s_hi = min(s_lo + pl.sc, p.S);
   const int nt = MODE == SCAN_SCORES ? (p.NV + N - 1) / N : (p.Nq + pl.PT - 1) / pl.PT;
-  auto key0 = [&](int kt) { return (batch + kt * pl.nb) * BM; };   // first key of key tile kt
-  // A causal key tile starts at the first query tile that sees its first key,
-  // the CTA at its first key tile's; nt where the slice has no such keys.
-  auto first_tile = [&](int kt, int n) {
-    const long long j = (long long)batch * BM + (long long)kt * pl.nb * BM;
-    if (j >= n) return nt;
-    return MODE == SCAN_WEIGHTS && p.causal ? min(nt, max(0, (int)j - (n - p.Nq)) / pl.PT) : 0;
+  // This batch's key tiles, at most NT of them
+  const int tile0 = (int)((long long)batch * pl.tiles / pl.nb);
+  const int tile_end = (int)((long long)(batch + 1) * pl.tiles / pl.nb);
+  const int j0 = tile0 * BM;                                       // its first key
+  // The query tiles it takes of a slice of n entries: under a causal limit
+  // from the first one that sees its first key on; none where n <= j0.
+  auto first_tile = [&](int n) {
+    if (j0 >= n) return nt;
+    return MODE == SCAN_WEIGHTS && p.causal ? min(nt, max(0, j0 - (n - p.Nq)) / pl.PT) : 0;
   };
-  if (MODE == SCAN_WEIGHTS && first_tile(0, ks_entries<MODE>(p, s_lo)) == nt && p.decay == 1.f) return;   // nothing to add
-  if (MODE == SCAN_WEIGHTS && key0(0) >= ks_entries<MODE>(p, s_lo)) return;
+  auto key_tiles = [&](int n) { return min(tile_end - tile0, (n - j0 + BM - 1) / BM); };   // for n > j0
+  if (MODE == SCAN_WEIGHTS && j0 >= ks_entries<MODE>(p, s_lo)) return;
 
   if (tid == 0) {
     mbar_init(key_full, Sh::NEPI * 32);
@@ -806,7 +924,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
       mbar_init(l_full + i, 1);
       mbar_init(l_empty + i, Sh::NEPI);
     }
-    for (int i = 0; i < NB * NT; ++i) {
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 4);
     }
@@ -836,17 +954,16 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     const int kt = warp >> 2;                              // this warpgroup's key tile
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const int e = tid & 127;
-    const long long jj = (long long)batch * BM + (long long)kt * pl.nb * BM + e;
-    const int j = jj < p.L ? (int)jj : p.L;                // past every slice's entries where there is none
+    const int j = kt < tile_end - tile0 ? j0 + kt * BM + e : p.L;   // past every entry where the batch has no such tile
     int* my_idx = idx + kt * BM;
     unsigned char* kdst = sm + kt * NK * Sh::KMAT;
     int loaded = -1, row = -1;
     float cs = p.c;
-    int round = 0, lround = 0;                             // accumulators and lse slots used so far
+    int seq = 0, lround = 0;                               // products of the CTA and lse slots so far
     bool ok = true;
     for (int s = s_lo; ok && s < s_hi; ++s) {
       const int n = ks_entries<MODE>(p, s);
-      const int t0 = first_tile(0, n), T = nt - t0, mine = first_tile(kt, n) - t0;
+      const int T = nt - first_tile(n);
       float* out = p.out + ((size_t)s * p.Hkv + g) * p.L;
       if (MODE == SCAN_SCORES && T == 0) {                 // no such blocks
         if (j < p.L) out[j] = -INF;
@@ -898,28 +1015,31 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
       float old = 0.f;
       if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldg(out + j);
       float total = MODE == SCAN_SCORES ? -INF : 0.f;
+      const int kn = T > 0 ? key_tiles(n) : 0;
       for (int t = 0; t < T; ++t) {
         const int sl = lround % NL;
         if (MODE == SCAN_WEIGHTS) {
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (lround / NL) & 1, abort_flag, wait_ns)))) break;
           ++lround;
-          if (t < mine) {   // these queries see none of the key tile
-            __syncwarp();
-            if (lane == 0) mbar_arrive(l_empty + sl);
-            continue;
-          }
         }
-        const int b = round % NB;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + kt * NB + b, (round / NB) & 1, abort_flag, wait_ns)))) break;
-        ++round;
+        const int mine_seq = seq + kt;
+        seq += kn;
+        if (kt >= kn) {   // no such key tile
+          __syncwarp();
+          if (MODE == SCAN_WEIGHTS && lane == 0) mbar_arrive(l_empty + sl);
+          continue;
+        }
+        const int b = mine_seq % NBUF;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (mine_seq / NBUF) & 1, abort_flag, wait_ns)))) break;
         tc_fence_after();
-        const uint32_t at = tbase + lanes + (kt * NB + b) * N;
+        const uint32_t at = tbase + lanes + b * N;
         const int m = p.NV - t * N;      // scores: real columns of the tile
-        const float4* l4 = reinterpret_cast<const float4*>(l2 + sl * N);
+        const float4* l4 = reinterpret_cast<const float4*>(nl2 + sl * N);
         const int4* m4 = reinterpret_cast<const int4*>(lim + sl * N);
         // this warp's highest key against the tile's first query
-        const bool masked = MODE == SCAN_WEIGHTS && (odd[sl] || (p.causal && key0(kt) + (warp & 3) * 32 + 31 > lim[sl * N]));
-        float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+        const bool masked = MODE == SCAN_WEIGHTS && (odd[sl] || (p.causal && j0 + kt * BM + (warp & 3) * 32 + 31 > lim[sl * N]));
+        float2 r0 = make_float2(0.f, 0.f), r1 = r0;
+        const float2 cs2 = make_float2(cs, cs);
         // 32 columns at a time, the next ones' load under way meanwhile
         uint32_t x[2][32];
         tmem_ld32(at, x[0]);
@@ -932,7 +1052,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty + kt * NB + b);
+            if (lane == 0) mbar_arrive(s_empty + b);
           }
           if constexpr (MODE == SCAN_SCORES) {
             if (m >= N) {
@@ -946,13 +1066,20 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
               }
             }
           } else if (!masked) {
+            // Two columns at a time; of 16 columns, 6 take the polynomial and 10 the
+            // exponential unit, which keeps both pipes busy.
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 l = l4[8 * c + i];
-              r0 += fast_ex2(fmaf(__uint_as_float(y[4 * i]), cs, -l.x));
-              r1 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 1]), cs, -l.y));
-              r2 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 2]), cs, -l.z));
-              r3 += fast_ex2(fmaf(__uint_as_float(y[4 * i + 3]), cs, -l.w));
+              const float2 a = __ffma2_rn(make_float2(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1])), cs2,
+                                          make_float2(l.x, l.y));
+              const float2 d = __ffma2_rn(make_float2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), cs2,
+                                          make_float2(l.z, l.w));
+              r0 = __fadd2_rn(r0, make_float2(fast_ex2(a.x), fast_ex2(a.y)));
+              if (i % 4 == 3)
+                r1 = __fadd2_rn(r1, make_float2(fast_ex2(d.x), fast_ex2(d.y)));
+              else
+                r1 = exp2_poly_add(d, r1);
             }
           } else {
 #pragma unroll
@@ -964,21 +1091,18 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
               float ev[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                const float ex = fast_ex2(fmaf(__uint_as_float(y[4 * i + u]), cs, -lv[u]));
-                ev[u] = lv[u] == INF ? 0.f : ex;
-                ev[u] = j <= mv[u] ? ev[u] : 0.f;
+                const float ex = fast_ex2(fmaf(__uint_as_float(y[4 * i + u]), cs, lv[u]));
+                ev[u] = lv[u] == -INF || j > mv[u] ? 0.f : ex;
               }
-              r0 += ev[0];
-              r1 += ev[1];
-              r2 += ev[2];
-              r3 += ev[3];
+              r0 = __fadd2_rn(r0, make_float2(ev[0], ev[1]));
+              r1 = __fadd2_rn(r1, make_float2(ev[2], ev[3]));
             }
           }
         }
         if (MODE == SCAN_WEIGHTS) {
           __syncwarp();
           if (lane == 0) mbar_arrive(l_empty + sl);
-          total += (r0 + r1) + (r2 + r3);
+          total += (r0.x + r0.y) + (r1.x + r1.y);
         }
       }
       if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
@@ -995,76 +1119,81 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     }
   } else if (warp == Sh::W_MMA) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const uint32_t id = make_idesc_f16(BM, N, bf16, false);
-      const uint64_t dK = sdesc_sw128(smem_u32(sm), 16, 1024);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
-      bool ok = true;
-      int loaded = -1, loads = 0, rounds[NT];
+    const uint32_t id = make_idesc_f16(BM, N, bf16, false);
+    const uint64_t dK = sdesc_sw128(smem_u32(sm), 16, 1024);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
+    bool ok = true;
+    int loaded = -1, loads = 0;
+    Ring qr, sr;
+    for (int s = s_lo; ok && s < s_hi; ++s) {
+      const int n = ks_entries<MODE>(p, s);
+      const int T = nt - first_tile(n);
+      if (T == 0 && MODE == SCAN_SCORES) continue;
+      const int kn = T > 0 ? key_tiles(n) : 0;
+      const int list = list_of_slice(s);
+      if (list != loaded) {
+        loaded = list;
+        ok = ks_poll(key_full, loads & 1, abort_flag, wait_ns);
+        ++loads;
+        fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
+      }
+      for (int t = 0; ok && t < T; ++t) {
 #pragma unroll
-      for (int kt = 0; kt < NT; ++kt) rounds[kt] = 0;
-      Ring qr;
-      for (int s = s_lo; ok && s < s_hi; ++s) {
-        const int n = ks_entries<MODE>(p, s);
-        const int t0 = first_tile(0, n), T = nt - t0;
-        if (MODE == SCAN_SCORES && T == 0) continue;
-        int mine[NT];
+        for (int m = 0; m < NK; ++m) {
+          const int st = qr.st;
+          ok = ok && ks_poll(q_full + st, qr.ph, abort_flag, wait_ns);
+          if (!ok) break;
+          qr.next(NST);
+          const uint64_t q = sdesc_at(dQ, st * Sh::QST);
 #pragma unroll
-        for (int kt = 0; kt < NT; ++kt) mine[kt] = first_tile(kt, n) - t0;
-        const int list = list_of_slice(s);
-        if (list != loaded) {
-          loaded = list;
-          ok = ks_poll(key_full, loads & 1, abort_flag, wait_ns);
-          ++loads;
-          fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
-        }
-        for (int t = 0; ok && t < T; ++t) {
-#pragma unroll
-          for (int m = 0; m < NK; ++m) {
-            const int st = qr.st;
-            ok = ok && ks_poll(q_full + st, qr.ph, abort_flag, wait_ns);
-            if (!ok) break;
-            qr.next(NST);
-            const uint64_t q = sdesc_at(dQ, st * Sh::QST);
-#pragma unroll
-            for (int kt = 0; kt < NT; ++kt) {
-              if (t < mine[kt] || !ok) continue;
-              const int b = rounds[kt] % NB;
-              if (m == 0) ok = ks_poll(s_empty + kt * NB + b, ((rounds[kt] / NB) & 1) ^ 1, abort_flag, wait_ns);
-              if (!ok) continue;
-              tc_fence_after();
-              const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT);
+          for (int kt = 0; kt < NT; ++kt) {
+            if (kt >= kn || !ok) continue;
+            if (m == 0) ok = ks_poll(s_empty + sr.st, sr.ph ^ 1u, abort_flag, wait_ns);
+            if (!ok) continue;
+            tc_fence_after();
+            const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT);
+            if (elect_one()) {
 #pragma unroll
               for (int i = 0; i < D / 16; ++i)
-                mma_ss(tbase + (kt * NB + b) * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
+                mma_ss(tbase + sr.st * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
                        sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
-              if (m == NK - 1) {
-                tc_commit(s_full + kt * NB + b);
-                ++rounds[kt];
-              }
+              if (m == NK - 1) tc_commit(s_full + sr.st);
             }
-            if (!ok) break;
-            tc_commit(q_empty + st);
+            __syncwarp();
+            if (m == NK - 1) sr.next(NBUF);
           }
+          if (!ok) break;
+          if (elect_one()) tc_commit(q_empty + st);
+          __syncwarp();
         }
       }
+    }
+    if (elect_one()) {
       tc_commit(drain);
       ks_wait_drain(drain, 0);
     }
+    __syncwarp();
   } else if (MODE == SCAN_WEIGHTS) {
     // ------------------------------------------------------------ queries by TMA
     const int s = s_lo, n = ks_entries<MODE>(p, s), PT = pl.PT;
-    const int t0 = first_tile(0, n), T = nt - t0;
+    const int t0 = first_tile(n), T = nt - t0;
     unsigned pend = 0, par = 0;
-    auto lse_of = [&](int t, int v) {   // log2-unit lse of column v of query tile t; +inf: adds nothing
-      const int i = (t0 + t) * PT + v / p.G;
-      if (t >= T || v >= PT * p.G || i >= p.Nq) return INF;
-      const float l = __ldg(p.lse + ((size_t)s * p.Nq + i) * p.Hq + g * p.G + v % p.G);
-      return l == -INF ? INF : l * kLog2e;
-    };
-    float nl[N / 32];
+    // This lane's columns v = lane + 32 u of a query tile: query v / G, head v % G.
+    // The next tile's lse are loaded as they stand and looked at when it is that tile's turn.
+    const float* lse_at[N / 32];
+    int qi[N / 32];
+    float raw[N / 32];
 #pragma unroll
-    for (int u = 0; u < N / 32; ++u) nl[u] = lse_of(0, lane + 32 * u);
+    for (int u = 0; u < N / 32; ++u) {
+      const int v = lane + 32 * u;
+      qi[u] = v < PT * p.G ? t0 * PT + v / p.G : 0x3fffffff;   // past every query
+      lse_at[u] = p.lse + (size_t)s * p.Nq * p.Hq + g * p.G + v % p.G;
+    }
+    auto load_lse = [&]() {
+#pragma unroll
+      for (int u = 0; u < N / 32; ++u) raw[u] = __ldg(lse_at[u] + (size_t)min(qi[u], p.Nq - 1) * p.Hq);
+    };
+    load_lse();
     for (int t = 0; t < T; ++t) {
       const int st = t % NST, u2 = t / NST, sl = t % NL;
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty + st, (u2 & 1) ^ 1, abort_flag, wait_ns))) break;
@@ -1082,11 +1211,13 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
 #pragma unroll
       for (int u = 0; u < N / 32; ++u) {
         const int v = lane + 32 * u;
-        l2[sl * N + v] = nl[u];
-        lim[sl * N + v] = p.causal ? n - p.Nq + (t0 + t) * PT + v / p.G : 0x7fffffff;
-        hide = hide || !(nl[u] < INF);
-        nl[u] = lse_of(t + 1, v);
+        const float l = qi[u] >= p.Nq || raw[u] == -INF ? -INF : raw[u] * -kLog2e;
+        nl2[sl * N + v] = l;
+        lim[sl * N + v] = p.causal ? n - p.Nq + min(qi[u], p.Nq) : 0x7fffffff;
+        hide = hide || !(l > -INF);
+        if (qi[u] < 0x3fffffff) qi[u] += PT;
       }
+      load_lse();
       hide = __any_sync(0xffffffffu, hide);
       if (lane == 0) odd[sl] = hide;
       __syncwarp();
@@ -1116,7 +1247,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), (kp::Shape<D, M
     bool ok = true;
     Ring qr;
     for (int s = s_lo; ok && s < s_hi; ++s) {
-      if (first_tile(0, ks_entries<MODE>(p, s)) == nt) continue;
+      if (first_tile(ks_entries<MODE>(p, s)) == nt) continue;
       fetch(s, 0);
       for (int t = 0; ok && t < nt; ++t) {
 #pragma unroll
@@ -1173,9 +1304,11 @@ template <int D, int MODE, int KIND>
 cudaError_t ks_stream(const KeyScanParams& p, cudaStream_t st) {
   auto kern = keyscan_stream_kernel<D, MODE, KIND>;
   const KsLayout ly = ks_layout<D, MODE, KIND>(p.NV);
+  constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  if (ly.nst < 1 || (ks::kGroups<D, NK, QUANT> == 2 && ly.nst <= NK) || ly.total > 227 * 1024) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ks::SMEM_MAX);
   if (e != cudaSuccess) return e;
-  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
   CUtensorMap t0, t1;
   memset(&t0, 0, sizeof(t0));
   memset(&t1, 0, sizeof(t1));
@@ -1204,7 +1337,8 @@ cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
   memset(&pl, 0, sizeof(pl));
   pl.sc = 1;
   const int tiles = (p.L + ks::BM - 1) / ks::BM;
-  const long long slots = (long long)ks_sms() * Sh::CTAS;
+  pl.tiles = tiles;
+  const long long slots = ks_sms();
   if (MODE == SCAN_WEIGHTS) {
     pl.PT = Sh::N / p.G;
     const long long queries = (long long)p.S * p.Nq;
@@ -1217,19 +1351,27 @@ cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
       return cudaErrorInvalidValue;
     // Batches of at most NT key tiles per (slice, KV head): as many as fill
     // the rounds of CTAs that full batches would take, so that the last round
-    // is a full one of slightly smaller batches (16,384 keys of 8 heads: 38
-    // batches of 3 or 4 tiles in two rounds, not 32 of 4 in 1.7).
+    // is a full one of smaller batches.
     const long long units = (long long)p.S * p.Hkv;
     const int full = (tiles + Sh::NT - 1) / Sh::NT;
     const long long rounds = (units * full + slots - 1) / slots;
     const long long nb = rounds * slots / units;
     pl.nb = (int)(nb < full ? full : nb > tiles ? tiles : nb);
   } else {
-    // Slices that share a sequence share its staged bounds: as many of them
-    // per CTA as leave a CTA for every slot
+    // Slices that share a sequence share its staged bounds.  The number of
+    // slices a CTA walks is the one that gives the fewest query tiles per SM,
+    // with the staging and start of a CTA counted as five of them.
     pl.nb = tiles;
-    const long long units = (long long)p.Hkv * tiles;
-    while (pl.sc < 8 && units * ((p.S + 2 * pl.sc - 1) / (2 * pl.sc)) >= slots) pl.sc *= 2;
+    const long long units = (long long)p.Hkv * tiles, per_slice = (p.NV + Sh::N - 1) / Sh::N;
+    long long best = -1;
+    for (int sc = 1; sc <= p.S && sc <= 64; ++sc) {
+      const long long ctas = units * ((p.S + sc - 1) / sc);
+      const long long cost = (ctas + slots - 1) / slots * (sc * per_slice + 5);
+      if (best < 0 || cost < best) {
+        best = cost;
+        pl.sc = sc;
+      }
+    }
   }
   pl.chunks = (p.S + pl.sc - 1) / pl.sc;
   const long long grid = (long long)pl.nb * p.Hkv * pl.chunks;

@@ -259,3 +259,35 @@ def test_weights_report_an_expired_wait_and_recover(kv, Nq):
     finally:
         far.fa_set_wait_limit_ns(0)
     assert torch.equal(far.fa_rows_weights(q, kd, rows, p.scale, lse, k_scale=ks, workspace=ws, check_status=True), want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("L", [5, 128, 129])
+def test_weights_of_one_tile_slices(kv, L):
+    # every (slice, KV head) is one or two tiles: the query buffers change with nearly every tile
+    p, kd, ks, k64 = make(340 + L, kv, S=90, Nq=1, Hq=8, Hkv=8, D=128, R=1024, L=L)
+    p.kv_len = synth.rng(341).integers(0, L + 1, size=90).astype(np.int32)
+    p.kv_len[5:20] = 0
+    for _ in range(3):
+        check(p, kd, ks, k64)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f8"])
+@pytest.mark.parametrize("Nq,L,G", [(1500, 1700, 4), (900, 900, 1), (700, 3000, 7), (2048, 2500, 2), (2048, 16384, 4)])
+def test_weights_of_long_prompts(kv, Nq, L, G):
+    # many query tiles per key tile, key tiles that only late queries see
+    p, kd, ks, k64 = make(350 + Nq, kv, S=1, Nq=Nq, Hq=2 * G, Hkv=2, D=128, R=32768, L=L, causal=True, pad_frac=0.02)
+    q = dev_bits(p.q, p.dtype).double().view(Nq, 2, G, 128)
+    k = torch.from_numpy(k64[np.maximum(p.kv_rows[0], 0)]).cuda()                      # [L, 2, D]
+    x = p.scale * torch.einsum("ighd,jgd->gihj", q, k)
+    j, i = torch.arange(L, device="cuda"), torch.arange(Nq, device="cuda")
+    see = (j[None] <= L - Nq + i[:, None]) & (torch.from_numpy(p.kv_rows[0]).cuda() >= 0)[None]
+    x.masked_fill_(~see[None, :, None], -float("inf"))
+    lse = torch.logsumexp(x, -1)                                                       # [2, Nq, G]
+    want = torch.exp(x - lse[..., None]).nan_to_num(0.0).sum((1, 2))
+    lse32 = lse.permute(1, 0, 2).reshape(1, Nq, 2 * G).float().contiguous()
+    for _ in range(2):
+        got = far.fa_rows_weights(dev_bits(p.q, p.dtype), kd, torch.from_numpy(p.kv_rows).cuda(), p.scale, lse32, causal=True,
+                                  k_scale=ks, check_status=True)[0].double()
+        # each term: exponent error below 2^-23 * ((D + 8) * 8 + 60) ~ 1.4e-4 for |scale q k| sums below 8, |x| + |lse| below 30
+        assert ((got - want).abs() <= 1.4e-4 * want + 1e-35).all(), ((got - want).abs() / want.clamp(min=1e-30)).max()
