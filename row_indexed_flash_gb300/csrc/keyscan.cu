@@ -195,35 +195,6 @@ __device__ __forceinline__ bool elect_one() {
   return x != 0;
 }
 
-// sum + 2^x, two at a time, on the FMA pipe: the exponential unit gives 16
-// results a clock and SM, the FMA pipe 128 operations.  x = n + f with n the
-// nearest integer (added to and taken back from 1.5 * 2^23, whose low bits
-// then hold it; 127 more makes them 2^n's exponent field), 2^f on [-1/2, 1/2]
-// by a degree-5 polynomial, the least-maximum fit of the relative error
-// (7.5e-8; 2.0e-7 evaluated in fp32).  x is clamped to [-126, 128]: below, 2^x
-// counts as 2^-126; from 128 on the exponent field is infinity's.  A NaN goes through f.
-__device__ __forceinline__ float2 exp2_poly_add(float2 x, float2 sum) {
-  auto clamp = [](float v) {
-    float y;
-    asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(y) : "f"(v));
-    asm("min.NaN.f32 %0, %0, 0f43000000;" : "+f"(y));
-    return y;
-  };
-  x = make_float2(clamp(x.x), clamp(x.y));
-  const float M = 12583039.0f;   // 1.5 * 2^23 + 127
-  const float2 t = __fadd2_rn(x, make_float2(M, M));
-  const float2 r = __fadd2_rn(t, make_float2(-M, -M));
-  const float2 f = __fadd2_rn(x, make_float2(-r.x, -r.y));
-  auto c = [](float v) { return make_float2(v, v); };
-  float2 q = __ffma2_rn(f, c(0.0013276472f), c(0.0096755414f));
-  q = __ffma2_rn(q, f, c(0.055507133f));
-  q = __ffma2_rn(q, f, c(0.2402212f));
-  q = __ffma2_rn(q, f, c(0.69314697f));
-  q = __ffma2_rn(q, f, c(1.0000001f));
-  const float2 e = make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23));
-  return __ffma2_rn(q, e, sum);
-}
-
 // 16 bytes of pool codes -> 16-bit values of Q's type, as 16-byte words.
 template <int KIND>
 __device__ __forceinline__ void widen_chunk(const uint4& w, bool bf16, uint4 (&o)[KvChunk<KIND>::N / 8]) {
@@ -280,7 +251,8 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
   constexpr int KT = D / 64;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by an offset, so that the compiler still knows the pointer for a shared one (plain, not generic, loads)
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const KsLayout ly = ks_layout<D, MODE, KIND>(p.NV);
   const int N = ly.N, NST = ly.nst;   // two groups of key warps: NST > NK (see kGroups)
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + ly.off_bar);
@@ -821,12 +793,14 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
 //
 // A CTA owns up to NT tiles of 128 keys, so that each staged query tile is
 // used NT times; one warpgroup reduces each key tile (thread = key, as above)
-// while the tensor core is at the others.  NBUF accumulators go round in the
-// order of the products, one more than there are key tiles: a key tile's next
-// product does not wait for the reduction of its last.  (More accumulators
-// than key tiles also keep a warpgroup's wait within one phase of its barrier:
-// the product before in the same accumulator is older than the
-// warpgroup's own last one.)
+// while the tensor core is at the others.  The NBUF >= NT accumulators go round in
+// the order of the products (then the product before in the same accumulator
+// is no newer than the warpgroup's own last one, and its wait stays within
+// one phase of the barrier).  Measured for a 2,048-token chunk over 16,384
+// entries of 8 heads, D 128: NT 4 with 128 columns 230 us, NT 3 with a fourth
+// accumulator 247 us, NT 4 with five of 96 columns 272 us (a product costs the
+// issuing warp about the same whatever its columns), a polynomial for 3 of 8
+// exponentials 345 us.
 // Scores (two stages per query tile, for max(q, 0) and min(q, 0)) keep both
 // bounds of one key tile; a CTA walks several slices, and stages the bounds
 // again only where the slice is of another sequence.
@@ -837,11 +811,11 @@ namespace kp {
 template <int D, int MODE>
 struct Shape {
   static constexpr bool SC = MODE == SCAN_SCORES;
-  static constexpr int NT = SC ? 1 : D == 256 ? 2 : 3;      // key tiles
+  static constexpr int NT = SC ? 1 : D == 256 ? 2 : 4;      // key tiles
   static constexpr int N = D == 256 ? 64 : 128;             // query vectors per tile
   static constexpr int NBUF = 4;                            // accumulators
   static constexpr int NK = SC ? 2 : 1;                     // stages per query tile
-  static constexpr int NST = SC ? (D == 256 ? 2 : 4) : D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int NST = SC ? (D == 256 ? 2 : 4) : D == 64 ? 4 : 2;
   static constexpr int NL = 4;                              // query tiles whose lse are on chip
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
@@ -877,7 +851,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
   constexpr int BM = ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by an offset, so that the compiler still knows the pointer for a shared one (plain, not generic, loads)
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* key_full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
   uint64_t* q_full = key_full + 1;
   uint64_t* q_empty = q_full + NST;
@@ -1066,8 +1041,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
               }
             }
           } else if (!masked) {
-            // Two columns at a time; of 16 columns, 6 take the polynomial and 10 the
-            // exponential unit, which keeps both pipes busy.
+            // two columns at a time
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 l = l4[8 * c + i];
@@ -1076,10 +1050,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
               const float2 d = __ffma2_rn(make_float2(__uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3])), cs2,
                                           make_float2(l.z, l.w));
               r0 = __fadd2_rn(r0, make_float2(fast_ex2(a.x), fast_ex2(a.y)));
-              if (i % 4 == 3)
-                r1 = __fadd2_rn(r1, make_float2(fast_ex2(d.x), fast_ex2(d.y)));
-              else
-                r1 = exp2_poly_add(d, r1);
+              r1 = __fadd2_rn(r1, make_float2(fast_ex2(d.x), fast_ex2(d.y)));
             }
           } else {
 #pragma unroll
