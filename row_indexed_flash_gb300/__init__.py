@@ -164,6 +164,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream, device) -> int:
     if stream is None:
+        if device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -342,16 +344,20 @@ def _raise_expired(entry: str, wtensor, stream):
         raise FaRowsError(FA_ERR_WAIT_EXPIRED, f"{entry}: a pipeline wait ran out; the outputs are invalid")
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(device):
     """Context that makes ``device`` the current one (nothing to do when it is)."""
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _NOTHING
     return torch.cuda.device(device)
 
 
 def _same_device(device, *tensors):
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors must share one device ({t.device} and {device})")
 
 
@@ -366,15 +372,15 @@ def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, 
     if kv_rows.dtype != torch.int32 or kv_rows.dim() != 2 or kv_rows.shape[0] != S:
         raise ValueError("kv_rows must be int32 [S, L]")
     L = kv_rows.shape[1]
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (S, Nq, Hq):
+    if lse.dtype != torch.float32 or lse.shape != (S, Nq, Hq):
         raise ValueError("lse must be float32 [S, Nq, Hq]")
-    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (S,)):
+    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (S,)):
         raise ValueError("kv_len must be int32 [S]")
-    if mask is not None and (mask.dtype != torch.float32 or tuple(mask.shape) != (S, Nq, L)):
+    if mask is not None and (mask.dtype != torch.float32 or mask.shape != (S, Nq, L)):
         raise ValueError("mask must be float32 [S, Nq, L]")
     if acc is None:
         acc = torch.zeros((S, Hkv, L), dtype=torch.float32, device=q.device)
-    elif acc.dtype != torch.float32 or tuple(acc.shape) != (S, Hkv, L):
+    elif acc.dtype != torch.float32 or acc.shape != (S, Hkv, L):
         raise ValueError("acc must be float32 [S, Hkv, L]")
     _same_device(q.device, k, kv_rows, lse, acc, kv_len, mask, k_scale, workspace)
     a = fa_rows_args()
@@ -405,9 +411,9 @@ def fa_kv_evict(acc, kv_rows, kv_len, sinks: int, recent: int, k: int, *, out_le
     if acc.dtype != torch.float32 or acc.dim() != 3:
         raise ValueError("acc must be float32 [S, Hkv, L]")
     S, Hkv, L = acc.shape
-    if kv_rows.dtype != torch.int32 or tuple(kv_rows.shape) != (S, L):
+    if kv_rows.dtype != torch.int32 or kv_rows.shape != (S, L):
         raise ValueError("kv_rows must be int32 [S, L]")
-    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (S,)):
+    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (S,)):
         raise ValueError("kv_len must be int32 [S]")
     n = int(out_len) if out_len is not None else int(sinks) + int(recent) + int(k)
     dev = acc.device
@@ -415,7 +421,7 @@ def fa_kv_evict(acc, kv_rows, kv_len, sinks: int, recent: int, k: int, *, out_le
     def dest(t, shape, dtype, name):
         if t is None:
             return torch.empty(shape, dtype=dtype, device=dev)
-        if t.dtype != dtype or tuple(t.shape) != shape:
+        if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name} must be {dtype} {shape}")
         return t
 
@@ -437,10 +443,10 @@ def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None)
     (the first fill[i] rows of each; fill None: 64).  Returns (kmin, kmax)."""
     R, Hkv, Dk = k.shape
     D = Dk * (2 if k.dtype == torch.uint8 else 1)
-    if kmin.dtype != kmax.dtype or tuple(kmin.shape) != (R // 64, Hkv, D) or tuple(kmax.shape) != (R // 64, Hkv, D):
+    if kmin.dtype != kmax.dtype or kmin.shape != (R // 64, Hkv, D) or kmax.shape != (R // 64, Hkv, D):
         raise ValueError(f"kmin and kmax must be [R/64, Hkv, D] = {(R // 64, Hkv, D)} of one dtype")
     for t, name in ((pages, "pages"), (fill, "fill")):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(pages.shape) or t.dim() != 1):
+        if t is not None and (t.dtype != torch.int32 or t.shape != pages.shape or t.dim() != 1):
             raise ValueError(f"{name} must be int32 [n_pages]")
     if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
         if k_scale is None:
@@ -456,9 +462,9 @@ def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None)
 def _check_pages(S, page_table, seq_len, slice_seq):
     if page_table.dtype != torch.int32 or page_table.dim() != 2:
         raise ValueError("page_table must be int32 [n_seq, max_pages]")
-    if seq_len.dtype != torch.int32 or tuple(seq_len.shape) != (S,):
+    if seq_len.dtype != torch.int32 or seq_len.shape != (S,):
         raise ValueError("seq_len must be int32 [S]")
-    if slice_seq is not None and (slice_seq.dtype != torch.int32 or tuple(slice_seq.shape) != (S,)):
+    if slice_seq is not None and (slice_seq.dtype != torch.int32 or slice_seq.shape != (S,)):
         raise ValueError("slice_seq must be int32 [S]")
 
 
@@ -474,7 +480,7 @@ def fa_kv_block_scores(q, kmin, kmax, page_table, seq_len, *, slice_seq=None, ou
     n_seq, max_pages = page_table.shape
     if out is None:
         out = torch.empty((S, Hkv, max_pages), dtype=torch.float32, device=q.device)
-    elif out.dtype != torch.float32 or tuple(out.shape) != (S, Hkv, max_pages):
+    elif out.dtype != torch.float32 or out.shape != (S, Hkv, max_pages):
         raise ValueError("out must be float32 [S, Hkv, max_pages]")
     _same_device(q.device, kmin, kmax, page_table, seq_len, slice_seq, out, workspace)
     with _on(q.device):
@@ -501,11 +507,11 @@ def fa_kv_block_rows(score, page_table, seq_len, sink_blocks: int, recent_blocks
     L = 64 * (int(sink_blocks) + int(recent_blocks) + int(k)) if list_len is None else int(list_len)
     if out is None:
         out = torch.empty((S, Hkv, L), dtype=torch.int32, device=score.device)
-    elif out.dtype != torch.int32 or tuple(out.shape) != (S, Hkv, L):
+    elif out.dtype != torch.int32 or out.shape != (S, Hkv, L):
         raise ValueError("out must be int32 [S, Hkv, list_len]")
     if out_len is None:
         out_len = torch.empty((S, Hkv), dtype=torch.int32, device=score.device)
-    elif out_len.dtype != torch.int32 or tuple(out_len.shape) != (S, Hkv):
+    elif out_len.dtype != torch.int32 or out_len.shape != (S, Hkv):
         raise ValueError("out_len must be int32 [S, Hkv]")
     _same_device(score.device, page_table, seq_len, slice_seq, out, out_len)
     with _on(score.device):

@@ -11,94 +11,164 @@ namespace far {
 
 namespace {
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // ---------------------------------------------------------------------------
 // Bounds: kmin[page, g, d], kmax[page, g, d] over the page's first fill rows.
-// A page is 64 rows of Hkv * D contiguous elements, so a thread owns one
-// 16-byte column of it and walks rows; the 8 row groups of a CTA meet in
-// shared memory.  Rounded outward (exact for 16-bit pools).  A NaN key makes
-// its bounds NaN.
+// HBM-bound: each key is read once.  A page is 64 rows of Hkv * D contiguous
+// elements; a thread owns one 16-byte column of it and up to 8 of its rows, all
+// loaded before any is looked at, and a CTA's row groups meet in shared memory.
+// 16-bit pools are compared as they stand, two columns an instruction; codes
+// of quantised pools as code * scale in fp32 (exact), two rows a comparison,
+// rounded outward at the end.  A NaN key makes its bounds NaN.
 
 constexpr int kBndThreads = 256;
+constexpr int kBndRows = 8;   // rows per thread
 
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint16_t round16(float x, bool up, bool bf16) {
   if (bf16) return __bfloat16_as_ushort(up ? __float2bfloat16_ru(x) : __float2bfloat16_rd(x));
   return __half_as_ushort(up ? __float2half_ru(x) : __float2half_rd(x));
 }
+template <int KIND>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  if constexpr (KIND == KV_BF16) {
+    const __nv_bfloat162 y = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __half2 y = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+template <int KIND>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  if constexpr (KIND == KV_BF16) {
+    const __nv_bfloat162 y = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const __half2 y = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
 
 template <int KIND>
 __global__ void __launch_bounds__(kBndThreads) bounds_kernel(const BoundsParams p, int cx) {
-  constexpr int N = KvChunk<KIND>::N;
-  extern __shared__ float bsm[];   // [row group][cx][2 N]
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  constexpr int N = KvChunk<KIND>::N;            // elements of a column
+  constexpr int W = QUANT ? N : N / 2;           // words that hold one bound of a column
+  extern __shared__ uint32_t bsm[];              // [row group][cx][2 W (+ 1)]
   const int page = __ldg(p.pages + blockIdx.x);
   if (page < 0 || (long long)page >= p.n_pool_pages) return;
   const int fill = p.fill ? min(max(__ldg(p.fill + blockIdx.x), 0), kPage) : kPage;
   if (fill == 0) return;
   const int rb = kv_row_bytes<KIND>(p.D);
-  const int cpr = p.Hkv * rb / 16;                 // 16-byte columns of a row
+  const int cpr = p.Hkv * (rb / 16);             // 16-byte columns of a row
   const int x = threadIdx.x % cx, rg = threadIdx.x / cx, nrg = kBndThreads / cx;
   const int col = blockIdx.y * cx + x;
   const float INF = __int_as_float(0x7f800000);
-  float lo[N], hi[N];
+  uint32_t lo[W], hi[W];
 #pragma unroll
-  for (int t = 0; t < N; ++t) {
-    lo[t] = INF;
-    hi[t] = -INF;
+  for (int t = 0; t < W; ++t) {
+    lo[t] = QUANT ? 0x7f800000u : KIND == KV_BF16 ? 0x7f807f80u : 0x7c007c00u;   // +inf
+    hi[t] = lo[t] | (QUANT ? 0x80000000u : 0x80008000u);
   }
   if (col < cpr) {
-    const int g = col * 16 / rb, c = col - g * (rb / 16);
-    for (int r = rg; r < fill; r += nrg) {
-      float v[N];
-      kv_chunk<KIND>(p.k, p.k_scale, page * kPage + r, g, p.Hkv, p.D, c, v);
+    const char* src = static_cast<const char*>(p.k) + ((size_t)page * kPage * cpr + col) * 16;
+    const uint16_t* sc = QUANT ? p.k_scale + ((size_t)page * p.Hkv + col / (rb / 16)) * kPage : nullptr;
+    // rows rg, rg + nrg, ...; a row past the fill is replaced by row 0, which
+    // the bounds hold anyway
+    uint4 w[kBndRows];
+    unsigned short s16[kBndRows];
 #pragma unroll
-      for (int t = 0; t < N; ++t) {
-        lo[t] = min_nan(lo[t], v[t]);
-        hi[t] = max_nan(hi[t], v[t]);
+    for (int i = 0; i < kBndRows; ++i) {
+      const int r = rg + i * nrg < fill ? rg + i * nrg : 0;
+      w[i] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * cpr * 16));
+      if (QUANT) s16[i] = __ldg(sc + r);
+    }
+    if constexpr (QUANT) {
+#pragma unroll
+      for (int i = 0; i < kBndRows; i += 2) {
+        float a[N], b[N];
+        kv_codes<KIND>(w[i], a);
+        kv_codes<KIND>(w[i + 1], b);
+        const float sa = __half2float(__ushort_as_half(s16[i])), sb = __half2float(__ushort_as_half(s16[i + 1]));
+#pragma unroll
+        for (int t = 0; t < N; t += 2) {
+          const float2 va = __fmul2_rn(make_float2(a[t], a[t + 1]), make_float2(sa, sa));
+          const float2 vb = __fmul2_rn(make_float2(b[t], b[t + 1]), make_float2(sb, sb));
+          lo[t] = __float_as_uint(min3_nan(__uint_as_float(lo[t]), va.x, vb.x));
+          hi[t] = __float_as_uint(max3_nan(__uint_as_float(hi[t]), va.x, vb.x));
+          lo[t + 1] = __float_as_uint(min3_nan(__uint_as_float(lo[t + 1]), va.y, vb.y));
+          hi[t + 1] = __float_as_uint(max3_nan(__uint_as_float(hi[t + 1]), va.y, vb.y));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBndRows; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int t = 0; t < W; ++t) {
+          lo[t] = min2_nan<KIND>(lo[t], u[t]);
+          hi[t] = max2_nan<KIND>(hi[t], u[t]);
+        }
       }
     }
   }
-  float* mine = bsm + (size_t)threadIdx.x * (2 * N + 1);
+  uint32_t* mine = bsm + (size_t)threadIdx.x * (2 * W + 1);
 #pragma unroll
-  for (int t = 0; t < N; ++t) {
+  for (int t = 0; t < W; ++t) {
     mine[t] = lo[t];
-    mine[N + t] = hi[t];
+    mine[W + t] = hi[t];
   }
   __syncthreads();
-  // thread -> one element of one bound of the slab
-  for (int f = threadIdx.x; f < cx * N; f += kBndThreads) {
-    const int xx = f / N, t = f % N;
-    const int cc = blockIdx.y * cx + xx;
+  // one word of one column's bounds per thread, over the row groups that hold rows
+  const int groups = min(nrg, kPage);
+  for (int f = threadIdx.x; f < cx * W; f += kBndThreads) {
+    const int xx = f / W, t = f % W, cc = blockIdx.y * cx + xx;
     if (cc >= cpr) continue;
-    float l = INF, h = -INF;
-    for (int r = 0; r < nrg; ++r) {
-      const float* o = bsm + (size_t)(r * cx + xx) * (2 * N + 1);
-      l = min_nan(l, o[t]);
-      h = max_nan(h, o[N + t]);
+    uint32_t l = bsm[(size_t)xx * (2 * W + 1) + t], h = bsm[(size_t)xx * (2 * W + 1) + W + t];
+    for (int r = 1; r < groups; ++r) {
+      const uint32_t* o = bsm + (size_t)(r * cx + xx) * (2 * W + 1);
+      if constexpr (QUANT) {
+        l = __float_as_uint(min3_nan(__uint_as_float(l), __uint_as_float(o[t]), INF));
+        h = __float_as_uint(max3_nan(__uint_as_float(h), __uint_as_float(o[W + t]), -INF));
+      } else {
+        l = min2_nan<KIND>(l, o[t]);
+        h = max2_nan<KIND>(h, o[W + t]);
+      }
     }
-    const size_t at = (size_t)page * p.Hkv * p.D + (size_t)cc * N + t;
-    static_cast<uint16_t*>(p.kmin)[at] = round16(l, false, p.out_bf16);
-    static_cast<uint16_t*>(p.kmax)[at] = round16(h, true, p.out_bf16);
+    const size_t at = ((size_t)page * cpr + cc) * W + t;   // words of 2 (16-bit pools) or elements
+    if constexpr (QUANT) {
+      static_cast<uint16_t*>(p.kmin)[at] = round16(__uint_as_float(l), false, p.out_bf16);
+      static_cast<uint16_t*>(p.kmax)[at] = round16(__uint_as_float(h), true, p.out_bf16);
+    } else {
+      static_cast<uint32_t*>(p.kmin)[at] = l;
+      static_cast<uint32_t*>(p.kmax)[at] = h;
+    }
   }
 }
 
 template <int KIND>
 cudaError_t bounds_kind(const BoundsParams& p, cudaStream_t st) {
-  const int cpr = p.Hkv * kv_row_bytes<KIND>(p.D) / 16;
-  int cx = 1;
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  constexpr int W = QUANT ? KvChunk<KIND>::N : KvChunk<KIND>::N / 2;
+  const int cpr = p.Hkv * (kv_row_bytes<KIND>(p.D) / 16);
+  // columns of a CTA: 32, or the row's own number rounded up to a power of two
+  // (no fewer than 4: 64 row groups of one row each)
+  int cx = 4;
   while (cx < cpr && cx < 32) cx <<= 1;
   const dim3 grid(p.n_pages, (cpr + cx - 1) / cx);
-  const size_t smem = (size_t)kBndThreads * (2 * KvChunk<KIND>::N + 1) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(bounds_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = (size_t)kBndThreads * (2 * W + 1) * sizeof(uint32_t);
+  const cudaError_t e = once_per_device<2>([smem] {
+    return cudaFuncSetAttribute(bounds_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
   if (e != cudaSuccess) return e;
   bounds_kernel<KIND><<<grid, kBndThreads, smem, st>>>(p, cx);
   return cudaGetLastError();
@@ -106,8 +176,8 @@ cudaError_t bounds_kind(const BoundsParams& p, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Block rows: one CTA per (slice, KV head).  The k-th largest key among the
-// middle blocks by radix selection (four 8-bit digits, a histogram per warp),
-// then one ordered pass that writes the chosen blocks' rows.
+// middle blocks by histograms over the keys' range, then one ordered pass that
+// writes the chosen blocks' rows.
 
 constexpr int kBrThreads = 512;
 constexpr int kBrWarps = kBrThreads / 32;
@@ -116,13 +186,18 @@ constexpr int kBrCap = 32768;          // blocks whose keys are kept in shared m
 
 __global__ void __launch_bounds__(kBrThreads) block_rows_kernel(const BlockRowsParams p, int cap) {
   extern __shared__ uint32_t keys[];   // [cap]
-  __shared__ int hist[kBrWarps][256];
+  __shared__ int hist[kBrThreads];
+  __shared__ uint32_t ends[2];         // smallest and largest key of the middle
   __shared__ int warp_sums[kBrWarps];
-  __shared__ int state[2];
+  __shared__ int state[3];
   __shared__ int last_listed;          // whether the sequence's last block was chosen
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.x, s = blockIdx.y;
-  if (tid == 0) last_listed = 0;
+  if (tid == 0) {
+    last_listed = 0;
+    ends[0] = 0xffffffffu;
+    ends[1] = 0u;
+  }
   const int seq = p.slice_seq ? __ldg(p.slice_seq + s) : s;
   const bool seq_ok = seq >= 0 && seq < p.n_seq;
   const long long cap_rows = (long long)p.max_pages * kPage;
@@ -137,61 +212,39 @@ __global__ void __launch_bounds__(kBrThreads) block_rows_kernel(const BlockRowsP
   int32_t* out = p.kv_rows + ((size_t)s * p.Hkv + g) * p.list_len;
   auto key_at = [&](int b) { return b < cap ? keys[b] : score_key(__ldg(sc + b)); };
 
-  uint32_t T = 0xffffffffu;
-  int need_eq = 0;
+  KeyRange range = key_range(0u, 0u, kk);
   if (!take_all && kk > 0) {
-    for (int b = lo + tid; b < min(hi, cap); b += kBrThreads) keys[b] = score_key(__ldg(sc + b));
-    uint32_t prefix = 0u, mask = 0u;
-    int remaining = kk;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int t = lane; t < 256; t += 32) hist[warp][t] = 0;
+    __syncthreads();
+    uint32_t kmin = 0xffffffffu, kmax = 0u;
+    for (int b = lo + tid; b < hi; b += kBrThreads) {
+      const uint32_t key = score_key(__ldg(sc + b));
+      if (b < cap) keys[b] = key;
+      kmin = min(kmin, key);
+      kmax = max(kmax, key);
+    }
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    if (lane == 0) {
+      atomicMin(&ends[0], kmin);
+      atomicMax(&ends[1], kmax);
+    }
+    __syncthreads();
+    range = key_range(ends[0], ends[1], kk);
+    while (!range.done) {
+      hist[tid] = 0;
       __syncthreads();
+      const int shift = range_shift<kBrThreads>(range);
       for (int b = lo + tid; b < hi; b += kBrThreads) {
         const uint32_t key = key_at(b);
-        if ((key & mask) == prefix) atomicAdd(&hist[warp][(key >> shift) & 255u], 1);
+        if (in_range(range, key)) atomicAdd(&hist[(key - range.base) >> shift], 1);
       }
       __syncthreads();
-      // warp 0: the digit where the count from the top reaches `remaining`;
-      // lane l owns digits 8 (31 - l) .. 8 (31 - l) + 7
-      if (tid < 256) {
-        int t = 0;
-#pragma unroll
-        for (int w = 0; w < kBrWarps; ++w) t += hist[w][tid];
-        hist[0][tid] = t;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        const int b0 = 8 * (31 - lane);
-        int local = 0;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) local += hist[0][b0 + t];
-        int incl = local;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        int cum = incl - local;
-        if (cum < remaining && incl >= remaining) {
-          for (int t = 7; t >= 0; --t) {
-            const int c = hist[0][b0 + t];
-            if (cum + c >= remaining) {
-              state[0] = b0 + t;
-              state[1] = remaining - cum;
-              break;
-            }
-            cum += c;
-          }
-        }
-      }
-      __syncthreads();
-      prefix |= (uint32_t)state[0] << shift;
-      remaining = state[1];
-      mask |= 255u << shift;
+      range_pick<kBrThreads>(range, hist[kBrThreads - 1 - tid], warp_sums, state);
+      __syncthreads();   // state and hist may be written again
     }
-    T = prefix;
-    need_eq = remaining;
   }
+  const uint32_t T = range.T;
+  const int need_eq = range.need_eq;
 
   // chosen blocks in order; out_at = blocks listed before this step
   int out_at = 0, eq_seen = 0;
@@ -298,7 +351,8 @@ cudaError_t scores_launch(const ScoresParams& p, cudaStream_t st) {
 
 cudaError_t block_rows_launch(const BlockRowsParams& p, cudaStream_t st) {
   const int cap = p.max_pages < kBrCap ? p.max_pages : kBrCap;
-  cudaError_t e = cudaFuncSetAttribute(block_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBrCap * 4);
+  const cudaError_t e = once_per_device<1>(
+      [] { return cudaFuncSetAttribute(block_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBrCap * 4); });
   if (e != cudaSuccess) return e;
   block_rows_kernel<<<dim3(p.Hkv, p.S), kBrThreads, (size_t)cap * 4, st>>>(p, cap);
   return cudaGetLastError();

@@ -9,11 +9,10 @@
 //
 // One thread-block cluster per slice, each CTA owning a run of positions: one
 // pass over the totals leaves an order-preserving 32-bit key per position in
-// shared memory, a radix selection (four 8-bit digits) finds the k-th largest
-// key with the CTAs' histograms added through distributed shared memory, and
-// one ordered pass writes the results after the CTAs have exchanged their
-// counts.  Nothing but the kernel's own inputs is re-read, and no scratch in
-// global memory is needed.
+// shared memory, two or three histograms over the keys' range find the k-th
+// largest with the CTAs' histograms added through distributed shared memory,
+// and one ordered pass writes the results after the CTAs have exchanged their
+// counts.  No scratch in global memory is needed.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -48,16 +47,16 @@ __device__ __forceinline__ float total_of(const float* a, int Hkv, size_t stride
   return isfinite(hi) ? hi + lo : hi;
 }
 
-__global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams p, int cap) {
-  extern __shared__ uint32_t keys[];          // [cap] 0: not an entry
-  __shared__ int hist[kEvWarps][256];
-  __shared__ int digits[2][256];              // this CTA's histogram, by pass parity
+__global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams p, int cap, int vec) {
+  extern __shared__ uint32_t keys[];          // [cap] 0: not an entry; later the kept positions
+  __shared__ int hist[2][kEvThreads];         // this CTA's histogram, by pass parity
+  __shared__ uint32_t ends[2];                // smallest and largest key of this CTA's part of the middle
   __shared__ int warp_sums[kEvWarps];
-  __shared__ int state[2];
-  __shared__ int counts[4];                   // this CTA's kept, equal to the threshold, live
+  __shared__ int state[3];
+  __shared__ int counts[4];                   // this CTA's entries in the middle, kept, equal to the threshold, live
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int s = blockIdx.y;
   const int n = p.kv_len ? min(max(__ldg(p.kv_len + s), 0), p.L) : p.L;
   const int chunk = ((n + C - 1) / C + 31) & ~31;
@@ -70,82 +69,100 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   };
   auto key_at = [&](int t) { return t < cap ? keys[t] : make_key(p0 + t); };
 
-  for (int t = tid; t < min(cnt, cap); t += kEvThreads) keys[t] = make_key(p0 + t);
+  // ---- keys, and the middle's smallest, largest and number
+  if (tid == 0) {
+    ends[0] = 0xffffffffu;
+    ends[1] = 0u;
+    counts[0] = 0;
+  }
+  __syncthreads();
+  uint32_t kmin = 0xffffffffu, kmax = 0u;
+  int in_middle = 0;
+  auto note = [&](int t, uint32_t key) {
+    if (t < cap) keys[t] = key;
+    if (key != 0u && p0 + t >= lo && p0 + t < hi) {
+      kmin = min(kmin, key);
+      kmax = max(kmax, key);
+      ++in_middle;
+    }
+  };
+  if (vec) {
+    // four positions a thread, the loads of up to four heads in flight
+    for (int t = 4 * tid; t < cnt; t += 4 * kEvThreads) {
+      if (t + 4 <= cnt) {
+        const int4 r = __ldg(reinterpret_cast<const int4*>(rows + p0 + t));
+        const float4* a = reinterpret_cast<const float4*>(acc + p0 + t);
+        const size_t stride = (size_t)p.L / 4;
+        float hi4[4], lo4[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < p.Hkv; g += 4) {
+          float4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[u] = __ldg(a + (size_t)min(g + u, p.Hkv - 1) * stride);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (g + u >= p.Hkv) break;
+            const float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (g + u == 0) hi4[e] = x[e];
+              else add_exactly(hi4[e], lo4[e], x[e]);
+            }
+          }
+        }
+        const int rv[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          note(t + e, rv[e] >= 0 ? score_key(isfinite(hi4[e]) ? hi4[e] + lo4[e] : hi4[e]) : 0u);
+      } else {
+        for (int e = t; e < cnt; ++e) note(e, make_key(p0 + e));
+      }
+    }
+  } else {
+    for (int t = tid; t < cnt; t += kEvThreads) note(t, make_key(p0 + t));
+  }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  in_middle = __reduce_add_sync(0xffffffffu, in_middle);
+  if (lane == 0 && in_middle > 0) {
+    atomicMin(&ends[0], kmin);
+    atomicMax(&ends[1], kmax);
+    atomicAdd(&counts[0], in_middle);
+  }
+  cluster.sync();
+  int m = 0;   // entries of the middle
+  kmin = 0xffffffffu;
+  kmax = 0u;
+  for (int r = 0; r < C; ++r) {
+    const uint32_t* e = cluster.map_shared_rank(&ends[0], r);
+    kmin = min(kmin, e[0]);
+    kmax = max(kmax, e[1]);
+    m += cluster.map_shared_rank(&counts[0], r)[0];
+  }
 
   // ---- the k-th largest key of the middle's entries
-  uint32_t prefix = 0u, mask = 0u;
-  int remaining = p.k;
-  bool take_all = false;
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int t = lane; t < 256; t += 32) hist[warp][t] = 0;
+  const bool take_all = m <= p.k, some = !take_all && p.k > 0;
+  KeyRange range = key_range(kmin, kmax, p.k);
+  for (int pass = 0; some && !range.done; ++pass) {
+    int* mine = hist[pass & 1];
+    mine[tid] = 0;
     __syncthreads();
+    const int shift = range_shift<kEvThreads>(range);
     for (int t = tid; t < cnt; t += kEvThreads) {
       const int pos = p0 + t;
       const uint32_t key = key_at(t);
-      if (key != 0u && pos >= lo && pos < hi && (key & mask) == prefix) atomicAdd(&hist[warp][(key >> shift) & 255u], 1);
+      if (key != 0u && pos >= lo && pos < hi && in_range(range, key)) atomicAdd(&mine[(key - range.base) >> shift], 1);
     }
-    __syncthreads();
-    if (tid < 256) {
-      int t = 0;
-#pragma unroll
-      for (int w = 0; w < kEvWarps; ++w) t += hist[w][tid];
-      digits[pass & 1][tid] = t;
-    }
-    cluster.sync();
-    // a CTA writes digits[parity] again two passes on, after a cluster barrier
+    // A CTA clears this histogram again two passes on, after a cluster barrier
     // that every reader of this pass has reached
-    if (tid < 256) {
-      int t = 0;
-      for (int r = 0; r < C; ++r) t += cluster.map_shared_rank(&digits[pass & 1][0], r)[tid];
-      hist[0][tid] = t;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l owns digits 8 (31 - l) .. 8 (31 - l) + 7
-      const int b0 = 8 * (31 - lane);
-      int local = 0;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) local += hist[0][b0 + t];
-      int incl = local;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const int all = __shfl_sync(0xffffffffu, incl, 31);
-      int cum = incl - local;
-      if (pass == 0 && all <= remaining) {   // every entry of the middle is kept
-        if (lane == 0) state[0] = -1;
-      } else if (cum < remaining && incl >= remaining) {
-        for (int t = 7; t >= 0; --t) {
-          const int c = hist[0][b0 + t];
-          if (cum + c >= remaining) {
-            state[0] = b0 + t;
-            state[1] = remaining - cum;
-            break;
-          }
-          cum += c;
-        }
-      } else if (remaining == 0 && lane == 0) {
-        state[0] = -2;
-      }
-    }
-    __syncthreads();
-    const int digit = state[0];
-    __syncthreads();
-    if (digit < 0) {
-      take_all = digit == -1;
-      break;
-    }
-    prefix |= (uint32_t)digit << shift;
-    remaining = state[1];
-    mask |= 255u << shift;
-    if (pass == 3) break;
+    cluster.sync();
+    int c = 0;
+#pragma unroll 4
+    for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(mine, r)[kEvThreads - 1 - tid];
+    range_pick<kEvThreads>(range, c, warp_sums, state);
+    __syncthreads();   // state may be written again
   }
-  const bool some = mask == 0xffffffffu;
-  const uint32_t T = some ? prefix : 0xffffffffu;
-  const int need_eq = some ? remaining : 0;
+  const uint32_t T = range.T;
+  const int need_eq = range.need_eq;
   // 0: dropped, 1: kept, 2: kept if among the first need_eq equal ones
   auto verdict = [&](int pos, uint32_t key) {
     if (key == 0u) return 0;
@@ -163,24 +180,23 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     c_eq += v == 2;
     c_live += key != 0u;
   }
-  if (tid < 4) counts[tid] = 0;
+  if (tid < 4) warp_sums[tid] = 0;
   __syncthreads();
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    c_keep += __shfl_xor_sync(0xffffffffu, c_keep, o);
-    c_eq += __shfl_xor_sync(0xffffffffu, c_eq, o);
-    c_live += __shfl_xor_sync(0xffffffffu, c_live, o);
-  }
+  c_keep = __reduce_add_sync(0xffffffffu, c_keep);
+  c_eq = __reduce_add_sync(0xffffffffu, c_eq);
+  c_live = __reduce_add_sync(0xffffffffu, c_live);
   if (lane == 0) {
-    atomicAdd(&counts[0], c_keep);
-    atomicAdd(&counts[1], c_eq);
-    atomicAdd(&counts[2], c_live);
+    atomicAdd(&warp_sums[0], c_keep);
+    atomicAdd(&warp_sums[1], c_eq);
+    atomicAdd(&warp_sums[2], c_live);
   }
+  __syncthreads();
+  if (tid < 3) counts[1 + tid] = warp_sums[tid];   // counts[0] may still be read by other CTAs
   cluster.sync();
   int out_at = 0, eq_seen = 0, live_before = 0, n_keep = 0, n_eq_all = 0, n_live = 0;
   for (int r = 0; r < C; ++r) {
     const int* c = cluster.map_shared_rank(&counts[0], r);
-    const int a = c[0], e = c[1], l = c[2];
+    const int a = c[1], e = c[2], l = c[3];
     if (r < rank) {
       out_at += a;
       eq_seen += e;
@@ -199,6 +215,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   int32_t* kept = p.kept ? p.kept + (size_t)s * p.out_len : nullptr;
   int32_t* freed = p.freed ? p.freed + (size_t)s * p.L : nullptr;
   float* acc_out = p.acc_out + (size_t)s * p.Hkv * p.out_len;
+  const int out_first = out_at;
   for (int base = 0; base < cnt; base += kEvThreads * kEvPer) {
     const int t0 = base + tid * kEvPer;
     int v[kEvPer];
@@ -230,7 +247,13 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
       if ((sel >> u) & 1u) {
         rows_out[at] = __ldg(rows + pos);
         if (kept) kept[at] = pos;
-        for (int g = 0; g < p.Hkv; ++g) acc_out[(size_t)g * p.out_len + at] = __ldg(acc + (size_t)g * p.L + pos);
+        // Noted for the copy of the totals below, in the key's place: a kept
+        // entry's number is no larger than its position, and every key up to
+        // this step's end has been read.
+        if (at - out_first < cap)
+          keys[at - out_first] = (uint32_t)pos;
+        else
+          for (int g = 0; g < p.Hkv; ++g) acc_out[(size_t)g * p.out_len + at] = __ldg(acc + (size_t)g * p.L + pos);
         ++at;
       } else if ((live >> u) & 1u) {
         if (freed) freed[dat] = __ldg(rows + pos);
@@ -240,6 +263,20 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     out_at += total & 0xffff;
     drop_at += total >> 16;
     eq_seen += eq_total;
+  }
+  __syncthreads();
+  // ---- the kept entries' totals: neighbouring threads, neighbouring outputs
+  const int mine_kept = min(out_at - out_first, cap);
+  for (int i = tid; i < mine_kept; i += kEvThreads) {
+    const int pos = (int)keys[i];
+    for (int g = 0; g < p.Hkv; g += 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = __ldg(acc + (size_t)min(g + u, p.Hkv - 1) * p.L + pos);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (g + u < p.Hkv) acc_out[(size_t)(g + u) * p.out_len + out_first + i] = v[u];
+    }
   }
   // ---- padding, spread over the cluster
   const int step = C * kEvThreads, me = rank * kEvThreads + tid;
@@ -263,9 +300,13 @@ cudaError_t evict_launch(const EvictParams& p, int sm_count, cudaStream_t st) {
   while (C < kEvMaxCluster && p.L > C * 2048 && (long long)p.S * C * 2 <= sm_count) C *= 2;
   const int chunk = ((p.L + C - 1) / C + 31) & ~31;
   const int cap = chunk < kEvCap ? chunk : kEvCap;
-  cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvCap * 4);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = once_per_device<0>([] {
+    cudaError_t x = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvCap * 4);
+    return x == cudaSuccess ? cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : x;
+  });
   if (e != cudaSuccess) return e;
+  // 16-byte loads of the totals and rows
+  const int vec = p.L % 4 == 0 && reinterpret_cast<uintptr_t>(p.acc) % 16 == 0 && reinterpret_cast<uintptr_t>(p.kv_rows) % 16 == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, p.S);
   cfg.blockDim = dim3(kEvThreads);
@@ -278,7 +319,7 @@ cudaError_t evict_launch(const EvictParams& p, int sm_count, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, p, cap);
+  return cudaLaunchKernelEx(&cfg, evict_kernel, p, cap, vec);
 }
 
 }  // namespace far

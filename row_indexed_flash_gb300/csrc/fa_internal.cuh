@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/fa_rows.h"
 
 namespace far {
@@ -148,6 +150,19 @@ cudaError_t launch_sparse_rows_ws(const float* score, int n_max, const int32_t* 
                                   cudaStream_t st);
 cudaError_t launch_validate(const int32_t* rows, const int32_t* kv_len, int S, int L, long long R,
                             long long* status, cudaStream_t st);
+
+// Runs f (which returns a cudaError_t, such as the setting of a kernel's
+// attributes) once per device and place in the code; repeated until it succeeds.
+template <int PLACE, class F>
+inline cudaError_t once_per_device(F f) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return f();
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = f();
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 // ---------------------------------------------------------------------------
 // small device helpers shared by the kernels of this library

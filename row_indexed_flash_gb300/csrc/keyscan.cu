@@ -1278,7 +1278,8 @@ cudaError_t ks_stream(const KeyScanParams& p, cudaStream_t st) {
   constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
   if (ly.nst < 1 || (ks::kGroups<D, NK, QUANT> == 2 && ly.nst <= NK) || ly.total > 227 * 1024) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ks::SMEM_MAX);
+  const cudaError_t e = once_per_device<3>(
+      [kern] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ks::SMEM_MAX); });
   if (e != cudaSuccess) return e;
   CUtensorMap t0, t1;
   memset(&t0, 0, sizeof(t0));
@@ -1300,7 +1301,8 @@ template <int D, int MODE, int KIND>
 cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
   using Sh = kp::Shape<D, MODE>;
   auto kern = keyscan_prompt_kernel<D, MODE, KIND>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  const cudaError_t e = once_per_device<4>(
+      [kern] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM); });
   if (e != cudaSuccess) return e;
   CUtensorMap tq;
   memset(&tq, 0, sizeof(tq));

@@ -41,4 +41,65 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   return before + x - v;
 }
 
+// Selection of the k-th largest of many 32-bit keys by histograms over the
+// keys' own range: the range [base, base + 2^bits) of the keys still in
+// question is cut into NT bins, the bin that holds the k-th largest becomes
+// the next range.  Cutting the range that is there, not fixed digits of the
+// key, spreads the first histogram (the upper digits of float scores are
+// nearly all alike, and their atomics would queue), so that two or three
+// passes do.
+struct KeyRange {
+  uint32_t base;   // first key of the range
+  int bits;        // its width: keys with (key - base) >> bits == 0
+  int left;        // how many of its keys, from the top, are still to take
+  bool done;       // threshold and need_eq are final
+  uint32_t T;      // keys above T are taken ...
+  int need_eq;     // ... and the first need_eq equal to it
+};
+
+__device__ __forceinline__ KeyRange key_range(uint32_t kmin, uint32_t kmax, int k) {
+  KeyRange r;
+  r.base = kmin;
+  r.bits = 32 - __clz((int)(kmax - kmin));
+  r.left = k;
+  r.done = false;
+  r.T = 0xffffffffu;
+  r.need_eq = 0;
+  return r;
+}
+template <int NT>
+__device__ __forceinline__ int range_shift(const KeyRange& r) {
+  constexpr int LOG = NT == 1024 ? 10 : NT == 512 ? 9 : 8;
+  static_assert((1 << LOG) == NT, "bins");
+  return max(r.bits - LOG, 0);
+}
+__device__ __forceinline__ bool in_range(const KeyRange& r, uint32_t key) {
+  return r.bits >= 32 || ((key - r.base) >> r.bits) == 0u;
+}
+// Narrows the range to the bin where the count from the top reaches `left`.
+// Thread t brings the count of bin NT - 1 - t.  state: 3 ints of shared memory.
+template <int NT>
+__device__ __forceinline__ void range_pick(KeyRange& r, int count, int* warp_sums, int* state) {
+  int total;
+  const int above = block_scan<NT>(count, warp_sums, &total);
+  if (above < r.left && above + count >= r.left) {
+    state[0] = NT - 1 - (int)threadIdx.x;
+    state[1] = r.left - above;
+    state[2] = count;
+  }
+  __syncthreads();
+  const int shift = range_shift<NT>(r);
+  r.base += (uint32_t)state[0] << shift;
+  r.left = state[1];
+  r.bits = shift;
+  if (state[2] == r.left) {          // the whole bin: every key from base on
+    r.T = r.base - 1u;
+    r.done = true;
+  } else if (shift == 0) {           // one key value, some of its holders
+    r.T = r.base;
+    r.need_eq = r.left;
+    r.done = true;
+  }
+}
+
 }  // namespace far
