@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kBrThreads) block_rows_kernel(const BlockRowsP
   extern __shared__ uint32_t keys[];   // [cap]
   __shared__ int hist[kBrThreads];
   __shared__ uint32_t ends[2];         // smallest and largest key of the middle
-  __shared__ int warp_sums[kBrWarps];
+  __shared__ int warp_sums[kBrWarps + 1];
   __shared__ int state[3];
   __shared__ int last_listed;          // whether the sequence's last block was chosen
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

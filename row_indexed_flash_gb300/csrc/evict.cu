@@ -26,9 +26,9 @@ namespace far {
 
 namespace {
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kEvPer = 4;            // consecutive positions per thread and step
+constexpr int kEvPer = 8;            // consecutive positions per thread and step
 constexpr int kEvCap = 40960;        // positions per CTA whose keys are kept in shared memory
 constexpr int kEvMaxCluster = 16;
 
@@ -47,11 +47,19 @@ __device__ __forceinline__ float total_of(const float* a, int Hkv, size_t stride
   return isfinite(hi) ? hi + lo : hi;
 }
 
+// A position's key from global memory.  Not inlined: the loops that use it for
+// the rare positions beyond the on-chip keys stay short (a launch runs its code
+// only a few times, so instruction fetches count).
+__device__ __noinline__ uint32_t key_from_memory(const float* acc, const int32_t* rows, int pos, int Hkv, int L) {
+  return __ldg(rows + pos) >= 0 ? score_key(total_of(acc + pos, Hkv, L)) : 0u;
+}
+
 __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams p, int cap, int vec) {
   extern __shared__ uint32_t keys[];          // [cap] 0: not an entry; later the kept positions
   __shared__ int hist[2][kEvThreads];         // this CTA's histogram, by pass parity
   __shared__ uint32_t ends[2];                // smallest and largest key of this CTA's part of the middle
-  __shared__ int warp_sums[kEvWarps];
+  __shared__ int warp_sums[kEvWarps + 1];
+  __shared__ int all[5];                      // the cluster's sums, or what lies before this CTA
   __shared__ int state[3];
   __shared__ int counts[4];                   // this CTA's entries in the middle, kept, equal to the threshold, live
   cg::cluster_group cluster = cg::this_cluster();
@@ -64,9 +72,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   const int lo = min(p.sinks, n), hi = max(lo, n - p.recent);   // the middle: [lo, hi)
   const float* acc = p.acc + (size_t)s * p.Hkv * p.L;
   const int32_t* rows = p.kv_rows + (size_t)s * p.L;
-  auto make_key = [&](int pos) {
-    return __ldg(rows + pos) >= 0 ? score_key(total_of(acc + pos, p.Hkv, p.L)) : 0u;
-  };
+  auto make_key = [&](int pos) { return key_from_memory(acc, rows, pos, p.Hkv, p.L); };
   auto key_at = [&](int t) { return t < cap ? keys[t] : make_key(p0 + t); };
 
   // ---- keys, and the middle's smallest, largest and number
@@ -87,19 +93,19 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     }
   };
   if (vec) {
-    // four positions a thread, the loads of up to four heads in flight
+    // four positions a thread, the loads of up to eight heads in flight
     for (int t = 4 * tid; t < cnt; t += 4 * kEvThreads) {
       if (t + 4 <= cnt) {
         const int4 r = __ldg(reinterpret_cast<const int4*>(rows + p0 + t));
         const float4* a = reinterpret_cast<const float4*>(acc + p0 + t);
         const size_t stride = (size_t)p.L / 4;
         float hi4[4], lo4[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int g = 0; g < p.Hkv; g += 4) {
-          float4 v[4];
+        for (int g = 0; g < p.Hkv; g += 8) {
+          float4 v[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = __ldg(a + (size_t)min(g + u, p.Hkv - 1) * stride);
+          for (int u = 0; u < 8; ++u) v[u] = __ldg(a + (size_t)min(g + u, p.Hkv - 1) * stride);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < 8; ++u) {
             if (g + u >= p.Hkv) break;
             const float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
@@ -129,15 +135,24 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     atomicAdd(&counts[0], in_middle);
   }
   cluster.sync();
-  int m = 0;   // entries of the middle
-  kmin = 0xffffffffu;
-  kmax = 0u;
-  for (int r = 0; r < C; ++r) {
-    const uint32_t* e = cluster.map_shared_rank(&ends[0], r);
-    kmin = min(kmin, e[0]);
-    kmax = max(kmax, e[1]);
-    m += cluster.map_shared_rank(&counts[0], r)[0];
+  if (tid < 32) {   // lane r reads CTA r
+    const bool there = lane < C;
+    const uint32_t* e = cluster.map_shared_rank(&ends[0], there ? lane : 0);
+    const uint32_t e0 = e[0], e1 = e[1];
+    const int c = cluster.map_shared_rank(&counts[0], there ? lane : 0)[0];
+    kmin = __reduce_min_sync(0xffffffffu, there ? e0 : 0xffffffffu);
+    kmax = __reduce_max_sync(0xffffffffu, there ? e1 : 0u);
+    const int sum = __reduce_add_sync(0xffffffffu, there ? c : 0);
+    if (lane == 0) {
+      all[0] = (int)kmin;
+      all[1] = (int)kmax;
+      all[2] = sum;
+    }
   }
+  __syncthreads();
+  kmin = (uint32_t)all[0];
+  kmax = (uint32_t)all[1];
+  const int m = all[2];   // entries of the middle
 
   // ---- the k-th largest key of the middle's entries
   const bool take_all = m <= p.k, some = !take_all && p.k > 0;
@@ -156,8 +171,9 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     // that every reader of this pass has reached
     cluster.sync();
     int c = 0;
-#pragma unroll 4
-    for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(mine, r)[kEvThreads - 1 - tid];
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r)
+      if (r < C) c += cluster.map_shared_rank(mine, r)[kEvThreads - 1 - tid];
     range_pick<kEvThreads>(range, c, warp_sums, state);
     __syncthreads();   // state may be written again
   }
@@ -165,10 +181,9 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   const int need_eq = range.need_eq;
   // 0: dropped, 1: kept, 2: kept if among the first need_eq equal ones
   auto verdict = [&](int pos, uint32_t key) {
-    if (key == 0u) return 0;
-    if (pos < lo || pos >= hi || take_all) return 1;
-    if (!some) return 0;
-    return key > T ? 1 : key == T ? 2 : 0;
+    const bool forced = take_all | (pos < lo) | (pos >= hi);
+    const int by_key = key > T ? 1 : key == T ? 2 : 0;
+    return key == 0u ? 0 : forced ? 1 : by_key;
   };
 
   // ---- this CTA's counts, exchanged
@@ -193,22 +208,26 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   __syncthreads();
   if (tid < 3) counts[1 + tid] = warp_sums[tid];   // counts[0] may still be read by other CTAs
   cluster.sync();
-  int out_at = 0, eq_seen = 0, live_before = 0, n_keep = 0, n_eq_all = 0, n_live = 0;
-  for (int r = 0; r < C; ++r) {
-    const int* c = cluster.map_shared_rank(&counts[0], r);
+  if (tid < 32) {
+    const bool there = lane < C, before = lane < rank;
+    const int* c = cluster.map_shared_rank(&counts[0], there ? lane : 0);
     const int a = c[1], e = c[2], l = c[3];
-    if (r < rank) {
-      out_at += a;
-      eq_seen += e;
-      live_before += l;
+    // sums over the CTAs before this one, and over all
+    const int v[6] = {__reduce_add_sync(0xffffffffu, before ? a : 0), __reduce_add_sync(0xffffffffu, before ? e : 0),
+                      __reduce_add_sync(0xffffffffu, before ? l : 0), __reduce_add_sync(0xffffffffu, there ? a : 0),
+                      __reduce_add_sync(0xffffffffu, there ? e : 0), __reduce_add_sync(0xffffffffu, there ? l : 0)};
+    if (lane == 0) {
+      const int kept_before = v[0] + min(v[1], need_eq);
+      all[0] = kept_before;
+      all[1] = v[1];
+      all[2] = v[2] - kept_before;
+      all[3] = v[3] + min(v[4], need_eq);
+      all[4] = v[5];
     }
-    n_keep += a;
-    n_eq_all += e;
-    n_live += l;
   }
-  out_at += min(eq_seen, need_eq);
-  n_keep += min(n_eq_all, need_eq);
-  int drop_at = live_before - out_at;
+  __syncthreads();
+  int out_at = all[0], eq_seen = all[1], drop_at = all[2];
+  const int n_keep = all[3], n_live = all[4];
 
   // ---- ordered pass
   int32_t* rows_out = p.rows_out + (size_t)s * p.out_len;
@@ -218,9 +237,12 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
   const int out_first = out_at;
   for (int base = 0; base < cnt; base += kEvThreads * kEvPer) {
     const int t0 = base + tid * kEvPer;
-    int v[kEvPer];
+    int v[kEvPer], row[kEvPer];
     unsigned live = 0u;
     int n_eq = 0;
+    // the rows that may be freed, loaded while the counts are formed
+#pragma unroll
+    for (int u = 0; u < kEvPer; ++u) row[u] = freed && t0 + u < cnt ? __ldg(rows + p0 + t0 + u) : -1;
 #pragma unroll
     for (int u = 0; u < kEvPer; ++u) {
       const uint32_t key = t0 + u < cnt ? key_at(t0 + u) : 0u;
@@ -245,18 +267,19 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     for (int u = 0; u < kEvPer; ++u) {
       const int pos = p0 + t0 + u;
       if ((sel >> u) & 1u) {
-        rows_out[at] = __ldg(rows + pos);
-        if (kept) kept[at] = pos;
-        // Noted for the copy of the totals below, in the key's place: a kept
-        // entry's number is no larger than its position, and every key up to
-        // this step's end has been read.
-        if (at - out_first < cap)
+        // Noted for the copy below, in a key's place: a kept entry's number is
+        // no larger than its position, and every key up to this step's end
+        // has been read.
+        if (at - out_first < cap) {
           keys[at - out_first] = (uint32_t)pos;
-        else
+        } else {
+          rows_out[at] = __ldg(rows + pos);
+          if (kept) kept[at] = pos;
           for (int g = 0; g < p.Hkv; ++g) acc_out[(size_t)g * p.out_len + at] = __ldg(acc + (size_t)g * p.L + pos);
+        }
         ++at;
       } else if ((live >> u) & 1u) {
-        if (freed) freed[dat] = __ldg(rows + pos);
+        if (freed) freed[dat] = row[u];
         ++dat;
       }
     }
@@ -265,10 +288,12 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
     eq_seen += eq_total;
   }
   __syncthreads();
-  // ---- the kept entries' totals: neighbouring threads, neighbouring outputs
+  // ---- the kept entries: neighbouring threads, neighbouring outputs
   const int mine_kept = min(out_at - out_first, cap);
   for (int i = tid; i < mine_kept; i += kEvThreads) {
     const int pos = (int)keys[i];
+    rows_out[out_first + i] = __ldg(rows + pos);
+    if (kept) kept[out_first + i] = pos;
     for (int g = 0; g < p.Hkv; g += 8) {
       float v[8];
 #pragma unroll

@@ -16,7 +16,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 // Exclusive prefix sum of v over a block of NT threads; *total gets the sum.
-// warp_sums: NT / 32 ints of shared memory.
+// warp_sums: NT / 32 + 1 ints of shared memory.
 template <int NT>
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   constexpr int NW = NT / 32;
@@ -29,16 +29,22 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int before = 0, sum = 0;
+  if (warp == 0) {
+    const int own = lane < NW ? warp_sums[lane] : 0;
+    int w = own;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const int t = warp_sums[w];
-    before += w < warp ? t : 0;
-    sum += t;
+    for (int o = 1; o < NW; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    if (lane < NW) warp_sums[lane] = w - own;
+    if (lane == NW - 1) warp_sums[NW] = w;
   }
-  *total = sum;
   __syncthreads();
-  return before + x - v;
+  const int before = warp_sums[warp] + x - v;
+  *total = warp_sums[NW];
+  __syncthreads();
+  return before;
 }
 
 // Selection of the k-th largest of many 32-bit keys by histograms over the
