@@ -11,10 +11,11 @@
 // heads sharing K/V ride in the MMA's M dimension and every K/V tile that is
 // staged serves all of them.  Per 128-entry KV tile j:
 //
-//   producer warp  TMA (3-D tensor map over the pool [R][Hkv][D]) when the 128
-//                  listed rows are one contiguous pool run, else a cp.async
-//                  gather into the same 128-byte-swizzled layout (padding
-//                  rows zero-filled); two K/V stages.
+//   producer warp  TMA (3-D tensor map over the pool [R][Hkv][D]) when each
+//                  half of the 128 listed rows is one contiguous pool run (a
+//                  long run, or two 64-row pages wherever they lie), else a
+//                  cp.async gather into the same 128-byte-swizzled layout
+//                  (padding rows zero-filled); two K/V stages.
 //   converters     (bf16 pools) two warps turn each landed V stage into f16
 //                  in place, so that P can be one f16 value: exact for every
 //                  bf16 value below 65536 in magnitude (one below 2^-14 becomes
@@ -121,17 +122,28 @@ __device__ __forceinline__ bool col_visible(int k, unsigned vb0, unsigned vb1, u
   return ((vb >> (k & 31)) & 1u) && (jbase + k <= lim);
 }
 
+// Whether each 64-row half of a tile is one contiguous pool run: lane l holds
+// rows l, l + 32, l + 64, l + 96 (-1: none); the halves' first rows in r0, r1.
+__device__ __forceinline__ bool half_runs(const int (&rows)[4], int lane, int& r0, int& r1) {
+  r0 = __shfl_sync(0xffffffffu, rows[0], 0);
+  r1 = __shfl_sync(0xffffffffu, rows[2], 0);
+  const bool run = r0 >= 0 && r1 >= 0 && rows[0] == r0 + lane && rows[1] == r0 + lane + 32 && rows[2] == r1 + lane &&
+                   rows[3] == r1 + lane + 32;
+  return __all_sync(0xffffffffu, run);
+}
+
 // MODE 0: f16 pool.  MODE 1: bf16 pool, V converted to f16 (f16 P).
 // MODE 2: bf16 pool, V kept in bf16 (the P pair).  A bf16 launch runs modes
 // 1 and 2; each CTA of the one the scan before the launch does not select
 // exits at once.  Mode 2 is selected when a listed V value is beyond f16's
-// range, or when more than a quarter of the KV tiles are gathered (not one
-// contiguous pool run): there mode 1 has a single warp gathering K (two
+// range, or when more than a quarter of the KV tiles are gathered (not
+// contiguous runs): there mode 1 has a single warp gathering K (two
 // gather and convert V), mode 2 three warps on both.
 template <int MODE>
 __global__ void __launch_bounds__(pf::NWARP * 32, 1)
     fa_rows_prefill_kernel(const PrefillKernelParams kp, const __grid_constant__ CUtensorMap tq,
-                           const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+                           const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                           const __grid_constant__ CUtensorMap tkh, const __grid_constant__ CUtensorMap tvh) {
   using namespace pf;
   constexpr bool BF16 = MODE != 0, VF16 = MODE == 1, PAIR = MODE == 2;
   const PrefillParams& p = kp.a;
@@ -229,11 +241,8 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
           const int pos = (j + 1) * BN + lane + 32 * t;
           nxt[t] = pos < n_s ? __ldg(rows_g + pos) : -1;
         }
-        const int r0 = __shfl_sync(0xffffffffu, rows[0], 0);
-        bool c = true;
-        #pragma unroll
-        for (int t = 0; t < 4; ++t) c = c && rows[t] >= 0 && rows[t] == r0 + lane + 32 * t;
-        contig = __all_sync(0xffffffffu, c) && kp.tma_kv;
+        int r0, r1;
+        contig = half_runs(rows, lane, r0, r1) && kp.tma_kv;
         if (!contig) {
           __syncwarp();
           #pragma unroll
@@ -299,8 +308,9 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
       cp_async_wait_all();
     } else if (warp == W_PROD || warp > W_MMA) {
       // ------------------------------------------------------------ producers
-      // Per KV tile: one TMA tile load per 64-column half and matrix when the
-      // 128 listed rows are one contiguous pool run (warp 8, lane 0), else a
+      // Per KV tile: one TMA tile load per 64-column half, 64-row half and
+      // matrix when both row halves are contiguous pool runs (the first
+      // producer warp, lane 0), else a
       // cp.async gather of the rows into the same 128-byte-swizzled layout
       // split over the three warps (padding rows zero-filled).  Every lane of
       // the three warps arrives once per stage and matrix; gather copies arrive
@@ -331,15 +341,22 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
       int nxt[4];
       #pragma unroll
       for (int t = 0; t < 4; ++t) nxt[t] = lane + 32 * t < n_s ? __ldg(rows_g + lane + 32 * t) : -1;
-      // one matrix of tile j into stage st: TMA tile loads for a contiguous
-      // run, else this warp's share of the gather; every lane arrives once
-      auto load = [&](bool contig, int r0, unsigned char* dst, const void* tmap, const char* src, uint64_t* full,
-                      int bit, int u) {
+      // one matrix of tile j into stage st: TMA tile loads for contiguous
+      // half tiles, else this warp's share of the gather; every lane arrives once
+      auto load = [&](bool contig, int r0, int r1, unsigned char* dst, const void* tmap, const void* tmap_half,
+                      const char* src, uint64_t* full, int bit, int u) {
         if (contig) {
           if (lead) {
             mbar_arrive_expect_tx(full, TILE);
-            tma_load_3d(dst, tmap, 0, g, r0, full);
-            tma_load_3d(dst + HALF, tmap, 64, g, r0, full);
+            // one run: boxes of 128 rows; two: boxes of 64, the second run's last
+            const bool whole = r1 == r0 + BN / 2;
+            const void* m = whole ? tmap : tmap_half;
+            tma_load_3d(dst, m, 0, g, r0, full);
+            tma_load_3d(dst + HALF, m, 64, g, r0, full);
+            if (!whole) {
+              tma_load_3d(dst + 64 * 128, m, 0, g, r1, full);
+              tma_load_3d(dst + HALF + 64 * 128, m, 64, g, r1, full);
+            }
             tma_pend |= 1u << bit;
             tma_par = (tma_par & ~(1u << bit)) | ((unsigned)(u & 1) << bit);
           } else {
@@ -366,11 +383,8 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
           const int pos = (j + 1) * BN + lane + 32 * t;
           nxt[t] = pos < n_s ? __ldg(rows_g + pos) : -1;
         }
-        const int r0 = __shfl_sync(0xffffffffu, rows[0], 0);
-        bool contig = true;
-        #pragma unroll
-        for (int t = 0; t < 4; ++t) contig = contig && rows[t] >= 0 && rows[t] == r0 + lane + 32 * t;
-        contig = __all_sync(0xffffffffu, contig) && kp.tma_kv;
+        int r0, r1;
+        const bool contig = half_runs(rows, lane, r0, r1) && kp.tma_kv;
         if (!contig) {
           // this warp's entries of the tile, for any lane to read (the region
           // is this warp's alone: another warp may already be on the next tile)
@@ -382,13 +396,13 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
         // K as soon as both QKs of tile j - NST have read the stage, V once both PVs have
         if (!__all_sync(0xffffffffu, mbar_wait(k_empty + st, (u & 1) ^ 1, abort_flag, wait_ns))) break;
         if (lead) tma_pend &= ~(1u << st);
-        load(contig, r0, sm + OFF_K + st * TILE, &tk, kb, k_full + st, st, u);
+        load(contig, r0, r1, sm + OFF_K + st * TILE, &tk, &tkh, kb, k_full + st, st, u);
         if (!__all_sync(0xffffffffu, mbar_wait(v_empty + st, (u & 1) ^ 1, abort_flag, wait_ns))) break;
         if (lead) tma_pend &= ~(1u << (NST + st));
         if (VF16 && !contig) {
           mbar_arrive(v_full + st);   // the converters gather this V tile
         } else {
-          load(contig, r0, sm + OFF_V + st * TILE, &tv, vb, v_full + st, NST + st, u);
+          load(contig, r0, r1, sm + OFF_V + st * TILE, &tv, &tvh, vb, v_full + st, NST + st, u);
         }
       }
       cp_async_wait_all();
@@ -717,13 +731,15 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
   if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
 }
 
-// Before a bf16 launch, per 128-entry KV tile of every list (one warp each):
-// is any listed V value finite and of magnitude 65536 or more (not an f16
-// value: word 1 of the status block gets 1), and is the tile not one
-// contiguous pool run (word 2 counts those, word 3 all tiles)?  The words
-// were zeroed before.  nl lists of which heads per slice (1: a list is read by
-// every KV head, so whole rows of row_chunks 16-byte chunks are examined; else
-// list l is read by head l % heads alone, and its row_chunks / heads chunks are).
+// Before a bf16 launch, per 128-entry KV tile of every list (a warp for each 32
+// of its entries: a warp for each tile left most SMs with three warps to wait
+// for memory with): is any listed V value finite and of magnitude 65536 or
+// more (not an f16 value: word 1 of the status block gets 1), and is the tile
+// not two contiguous half runs (word 2 counts those, word 3 all tiles)?  The
+// words were zeroed before.  nl lists; HEADS: list l is read by KV head
+// l % heads alone, and only that head's 256 bytes of each row are examined,
+// else every head reads it, and whole rows of row_chunks 16-byte chunks are.
+template <bool HEADS>
 __global__ void __launch_bounds__(256) prefill_v_scan_kernel(const uint4* v, const int32_t* kv_rows,
                                                              const int32_t* kv_len, int nl, int L, long long R,
                                                              int row_chunks, int heads, int tma_kv, unsigned int* words) {
@@ -732,58 +748,53 @@ __global__ void __launch_bounds__(256) prefill_v_scan_kernel(const uint4* v, con
   const long long nw = (long long)gridDim.x * (blockDim.x >> 5);
   uint32_t bad = 0;
   unsigned gathered = 0, tiles = 0;
-  for (long long e = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); e < (long long)nl * tiles_per;
-       e += nw) {
-    const int s = (int)(e / tiles_per), j0 = (int)(e % tiles_per) * pf::BN;
+  auto examine = [&](const uint4& w) {
+    const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t a = wv[q] & 0x7fff7fffu;
+      bad |= __vcmpgeu2(a, 0x47804780u) & __vcmpltu2(a, 0x7f807f80u);
+    }
+  };
+  for (long long e = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); e < 4ll * nl * tiles_per; e += nw) {
+    const int quarter = (int)(e & 3);
+    const int s = (int)((e >> 2) / tiles_per), j0 = (int)((e >> 2) % tiles_per) * pf::BN;
     const int n_s = kv_len ? min(max(__ldg(kv_len + s), 0), L) : L;
     if (j0 >= n_s) continue;
     const int32_t* rows = kv_rows + (size_t)s * L + j0;
-    const int c_lo = (s % heads) * (row_chunks / heads), c_hi = c_lo + row_chunks / heads;
-    int r[4];
-    #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int pos = lane + 32 * t;
+    auto entry = [&](int pos) {
       const int x = j0 + pos < n_s ? __ldg(rows + pos) : -1;
-      r[t] = (x < 0 || (long long)x >= R) ? -1 : x;
+      return (x < 0 || (long long)x >= R) ? -1 : x;
+    };
+    const int own = entry(quarter * 32 + lane);
+    if (quarter == 0) {
+      const int r[4] = {own, entry(lane + 32), entry(lane + 64), entry(lane + 96)};
+      int r0, r1;
+      ++tiles;
+      if (!(half_runs(r, lane, r0, r1) && tma_kv != 0)) ++gathered;
     }
-    const int r0 = __shfl_sync(0xffffffffu, r[0], 0);
-    bool contig = tma_kv != 0;
-    #pragma unroll
-    for (int t = 0; t < 4; ++t) contig = contig && r[t] >= 0 && r[t] == r0 + lane + 32 * t;
-    contig = __all_sync(0xffffffffu, contig);
-    ++tiles;
-    if (!contig) ++gathered;
-    // the tile's rows four at a time, each read by the whole warp (coalesced),
-    // all of a group's loads issued before any is examined
-    #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      for (int rr = 0; rr < 32; rr += 4) {
-        int row[4];
-        #pragma unroll
-        for (int u = 0; u < 4; ++u) row[u] = __shfl_sync(0xffffffffu, r[t], rr + u);
-        for (int i0 = c_lo; i0 < c_hi; i0 += 64) {
-          uint4 w[4][2];
+    uint4 w[16];
+    if constexpr (HEADS) {
+      // one row of 16 chunks per half warp, all 32 rows' loads issued before any is examined
+      const uint4* vh = v + (s % heads) * (pf::HD / 8) + (lane & 15);
+      #pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int row = __shfl_sync(0xffffffffu, own, 2 * u + (lane >> 4));
+        w[u] = row >= 0 ? __ldg(vh + (size_t)row * row_chunks) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      #pragma unroll
+      for (int u = 0; u < 16; ++u) examine(w[u]);
+    } else {
+      // eight rows at a time, each read by the whole warp, 1 KB of each
+      for (int rr = 0; rr < 32; rr += 8) {
+        for (int i0 = 0; i0 < row_chunks; i0 += 64) {
           #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int i = i0 + lane + 32 * c;
-              w[u][c] = (row[u] >= 0 && i < c_hi) ? __ldg(v + (size_t)row[u] * row_chunks + i)
-                                                        : make_uint4(0u, 0u, 0u, 0u);
-            }
+          for (int u = 0; u < 16; ++u) {
+            const int row = __shfl_sync(0xffffffffu, own, rr + (u >> 1)), i = i0 + (u & 1) * 32 + lane;
+            w[u] = (row >= 0 && i < row_chunks) ? __ldg(v + (size_t)row * row_chunks + i) : make_uint4(0u, 0u, 0u, 0u);
           }
           #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t wv[4] = {w[u][c].x, w[u][c].y, w[u][c].z, w[u][c].w};
-              #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t a = wv[q] & 0x7fff7fffu;
-                bad |= __vcmpgeu2(a, 0x47804780u) & __vcmpltu2(a, 0x7f807f80u);
-              }
-            }
-          }
+          for (int u = 0; u < 16; ++u) examine(w[u]);
         }
       }
     }
@@ -824,24 +835,31 @@ cudaError_t prefill_launch(const PrefillParams& a, cudaStream_t st) {
   kp.q_box = (int)(qrows < kp.PT ? qrows : kp.PT);
   kp.tma_kv = a.R >= pf::BN;
   const bool bf16 = a.is_bf16 != 0;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, tkh, tvh;
   memset(&tq, 0, sizeof(tq));
   memset(&tk, 0, sizeof(tk));
   memset(&tv, 0, sizeof(tv));
+  memset(&tkh, 0, sizeof(tkh));
+  memset(&tvh, 0, sizeof(tvh));
   if (!make_map_3d(&tq, a.q, bf16, pf::HD, a.Hq, (uint64_t)qrows, 64, a.G, kp.q_box)) return cudaErrorInvalidValue;
   if (kp.tma_kv) {
-    if (!make_map_3d(&tk, a.k, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN)) return cudaErrorInvalidValue;
-    if (!make_map_3d(&tv, a.v, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN)) return cudaErrorInvalidValue;
+    // boxes of a whole tile's rows, and of half a tile's
+    if (!make_map_3d(&tk, a.k, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN) ||
+        !make_map_3d(&tv, a.v, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN) ||
+        !make_map_3d(&tkh, a.k, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN / 2) ||
+        !make_map_3d(&tvh, a.v, bf16, pf::HD, a.Hkv, a.R, 64, 1, pf::BN / 2))
+      return cudaErrorInvalidValue;
   }
   if (bf16) {
     // words 1-3 of the status block: the scan's V-range flag, gathered and all KV tiles
     cudaError_t e = cudaMemsetAsync(a.err + 1, 0, 3 * sizeof(unsigned int), st);
     if (e != cudaSuccess) return e;
     const long long nl = a.head_lists ? (long long)a.S * a.Hkv : a.S;
-    const long long tiles = nl * ((a.L + pf::BN - 1) / pf::BN);   // one warp each, 8 per block
-    const long long blocks = (tiles + 7) / 8;
+    const long long tiles = nl * ((a.L + pf::BN - 1) / pf::BN);   // four warps each, 8 per block
+    const long long blocks = (tiles + 1) / 2;
     if (blocks > 0) {
-      prefill_v_scan_kernel<<<(unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(
+      auto scan = a.head_lists ? prefill_v_scan_kernel<true> : prefill_v_scan_kernel<false>;
+      scan<<<(unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(
           static_cast<const uint4*>(a.v), a.kv_rows, a.kv_len, (int)nl, a.L, a.R, a.Hkv * pf::HD / 8, a.head_lists ? a.Hkv : 1, kp.tma_kv,
           a.err + 1);
       e = cudaGetLastError();
@@ -865,7 +883,7 @@ cudaError_t prefill_launch(const PrefillParams& a, cudaStream_t st) {
       if (e != cudaSuccess) return e;
       attr_done[dev].fetch_or(bit, std::memory_order_relaxed);
     }
-    kern<<<grid, pf::NWARP * 32, pf::SMEM, st>>>(kp, tq, tk, tv);
+    kern<<<grid, pf::NWARP * 32, pf::SMEM, st>>>(kp, tq, tk, tv, tkh, tvh);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
