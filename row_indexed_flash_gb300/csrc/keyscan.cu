@@ -94,9 +94,10 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   l.off_k = (2 * l.qb_bytes + 1023) / 1024 * 1024;
   const int room = ks::SMEM_MAX - 1024 - l.off_k - 2048;
   if (QUANT) {
-    // two operand stages (one for D 256), the code ring
-    l.nst = D <= 128 ? 2 : 1;
+    // the code ring, operand stages with what is left (two at least; one for D 256)
     l.ncs = ks::kGroups<D, 1, true> * (ks_ahead<D, KIND>() + 1);
+    l.nst = (room - l.ncs * l.code) / l.tile;
+    l.nst = l.nst > ks::MAXST ? ks::MAXST : l.nst;
   } else {
     l.nst = room / l.tile;
     l.nst = l.nst > ks::MAXST ? ks::MAXST : l.nst;
@@ -565,18 +566,32 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(q_empty + qb, ((unit >> 1) & 1) ^ 1, abort_flag, wait_ns))) break;
       unsigned char* dst = sm + ly.off_q + qb * ly.qb_bytes;
       const uint16_t* qg = static_cast<const uint16_t*>(p.q);
-#pragma unroll 4
-      for (int f = lane; f < N * CPR; f += 32) {
-        const int v = f / CPR, c = f % CPR;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (v < p.NV)
-          x = __ldg(reinterpret_cast<const uint4*>(qg + (((size_t)w.s * p.Nq + v / p.G) * p.Hq + w.g * p.G + v % p.G) * D) + c);
-        unsigned char* at = dst + (size_t)(c >> 3) * N * 128 + v * 128 + (((c & 7) ^ (v & 7)) << 4);
-        if (MODE == SCAN_SCORES) {
-          *reinterpret_cast<uint4*>(at) = sign_part(x, true, bf16);
-          *reinterpret_cast<uint4*>(at + (size_t)KT * N * 128) = sign_part(x, false, bf16);
-        } else {
-          *reinterpret_cast<uint4*>(at) = x;
+      const uint16_t* base = qg + ((size_t)w.s * p.Nq * p.Hq + w.g * p.G) * D;
+      auto row_at = [&](int v) { return base + (size_t)(v / p.G * p.Hq + v % p.G) * D; };
+      if (MODE == SCAN_WEIGHTS) {
+        // all copies under way before the first is waited for: the first
+        // tile's products wait for them
+        for (int f = lane; f < N * CPR; f += 32) {
+          const int v = f / CPR, c = f % CPR;
+          cp_async16(dst + (c >> 3) * N * 128 + v * 128 + (((c & 7) ^ (v & 7)) << 4), row_at(min(v, p.NV - 1)) + c * 8, v < p.NV);
+        }
+      } else {
+        for (int f0 = 0; f0 < N * CPR; f0 += 8 * 32) {   // N * CPR is a multiple of 128
+          uint4 x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int f = min(f0 + u * 32 + lane, N * CPR - 1), v = f / CPR;
+            x[u] = __ldg(reinterpret_cast<const uint4*>(row_at(min(v, p.NV - 1))) + f % CPR);
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int f = f0 + u * 32 + lane, v = f / CPR, c = f % CPR;
+            if (f >= N * CPR) break;
+            if (v >= p.NV) x[u] = make_uint4(0u, 0u, 0u, 0u);
+            unsigned char* at = dst + (c >> 3) * N * 128 + v * 128 + (((c & 7) ^ (v & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = sign_part(x[u], true, bf16);
+            *reinterpret_cast<uint4*>(at + KT * N * 128) = sign_part(x[u], false, bf16);
+          }
         }
       }
       if (MODE == SCAN_WEIGHTS) {
@@ -585,6 +600,7 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
           l2[qb * MAXN + v] = l == -INF ? INF : l * kLog2e;
           lim[qb * MAXN + v] = w.n - p.Nq + v / p.G;
         }
+        cp_async_wait_all();
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -820,7 +836,7 @@ struct Shape {
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
   static constexpr int QST = N * D * 2;               // one query stage
-  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = SC ? 4 : 1;
+  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = SC ? 8 : 1;
   static constexpr int THREADS = (W_Q + NQW) * 32;
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
@@ -1203,16 +1219,35 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     constexpr int CPR = D / 8, STEP = Sh::NQW * 32, NX = N * CPR / STEP;
     const int qt = tid - Sh::W_Q * 32;
     const uint16_t* qg = static_cast<const uint16_t*>(p.q);
-    // this thread's 16-byte words of a query tile
+    // this thread's 16-byte words of a query tile, and the query rows
+    // (query * Hq + head) that they are of; where whole queries fill a tile,
+    // the next tile's rows are a fixed number further on
     uint4 x[NX];
-    auto fetch = [&](int s, int t) {
+    int at[NX];
+    const bool whole = N % p.G == 0;
+    const int pitch = N / p.G * p.Hq;
+    auto locate = [&](int t) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
-        const int f = i * STEP + qt, v = t * N + f / CPR;
-        const int vc = min(v, p.NV - 1);
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(
-                                  qg + (((size_t)s * p.Nq + vc / p.G) * p.Hq + g * p.G + vc % p.G) * D) + f % CPR);
-        x[i] = v < p.NV ? y : make_uint4(0u, 0u, 0u, 0u);
+        const int v = min(t * N + (i * STEP + qt) / CPR, p.NV - 1);
+        at[i] = v / p.G * p.Hq + v % p.G;
+      }
+    };
+    auto fetch = [&](int s, int t) {
+      if (t == 0 || !whole || (t + 1) * N > p.NV) {
+        locate(t);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) at[i] += pitch;
+      }
+      const uint16_t* base = qg + ((size_t)s * p.Nq * p.Hq + g * p.G) * D;
+#pragma unroll
+      for (int i = 0; i < NX; ++i)
+        x[i] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)at[i] * D) + (i * STEP + qt) % CPR);
+      if ((t + 1) * N > p.NV) {   // past the last query: zeros
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+          if (t * N + (i * STEP + qt) / CPR >= p.NV) x[i] = make_uint4(0u, 0u, 0u, 0u);
       }
     };
     bool ok = true;
