@@ -18,7 +18,7 @@
 //   8      MMA issue; allocates tensor memory
 //   9      queries of the next (slice, KV head), into one of two buffers: its
 //          rows and, for weights, lse in log2 units and the causal limits
-//   10-17  keys: two groups of four warps on alternate tiles (one group's
+//   10 on  keys: two groups of four warps (eight for codes) on alternate tiles (one group's
 //          instructions per tile take longer than the tile's share of HBM
 //          time), two warps for each 64-row half; cp.async of the listed rows
 //          into the 128-byte-swizzled layout, or one TMA tile load per 64
@@ -43,11 +43,14 @@ namespace far {
 
 namespace ks {
 constexpr int BM = 128;                    // keys per tile
-constexpr int NEPI = 8, W_MMA = 8, W_Q = 9, W_KEY = 10, NKEY = 8;
+constexpr int NEPI = 8, W_MMA = 8, W_Q = 9, W_KEY = 10;
+// Key warps: widening codes takes twice the warps that copies alone do.
+template <bool QUANT>
+constexpr int kKeyWarps = QUANT ? 16 : 8;
+template <bool QUANT>
+constexpr int kThreads = (W_KEY + kKeyWarps<QUANT>) * 32;
 constexpr int NBUF = 4;                    // accumulators
-constexpr int NWARP = W_KEY + NKEY;
-constexpr int THREADS = NWARP * 32;
-constexpr int MAXST = 8;
+constexpr int MAXST = 8;                  // stages
 constexpr int MAXN = kScanStreamVec;
 constexpr int PRE = 3;                     // own tiles ahead that a key warp loads list entries
 // Groups of key warps on alternate tiles: two, but one for the codes of D 256
@@ -242,12 +245,13 @@ __device__ __forceinline__ uint4 sign_part(const uint4& x, bool plus, bool bf16)
 }
 
 template <int D, int MODE, int KIND>
-__global__ void __launch_bounds__(ks::THREADS, 1)
+__global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8>, 1)
     keyscan_stream_kernel(const KeyScanParams p, int tma_ok, const __grid_constant__ CUtensorMap t0,
                           const __grid_constant__ CUtensorMap t1) {
   using namespace ks;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
   constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;   // stages per tile
+  constexpr int NKEY = kKeyWarps<QUANT>;
   constexpr int ATOM = BM * 128;                    // one 64-column atom of a key tile
   constexpr int KT = D / 64;
   const float INF = __int_as_float(0x7f800000);
@@ -735,12 +739,12 @@ __global__ void __launch_bounds__(ks::THREADS, 1)
           const int row = row_of(set), g = wi.g;
           unsigned char* dst = ring + slot * ly.code;
           if (++slot == NCS) slot = 0;
+          const char* src = static_cast<const char*>(p.k[0]) + (size_t)g * CB + lane % CPR * 16;   // 32 % CPR = 0
+          const size_t pitch = (size_t)p.Hkv * CB;
 #pragma unroll
           for (int it = 0; it < NIT; ++it) {
-            const int f = it * 32 + lane, e = f / CPR, c = f % CPR;
-            const int r = __shfl_sync(0xffffffffu, row, e);
-            const bool okr = r >= 0;
-            cp_async16(dst + f * 16, static_cast<const char*>(p.k[0]) + ((size_t)(okr ? r : 0) * p.Hkv + g) * CB + c * 16, okr);
+            const int r = __shfl_sync(0xffffffffu, row, it * (32 / CPR) + lane / CPR);
+            cp_async16(dst + (it * 32 + lane) * 16, src + (r >= 0 ? r : 0) * pitch, r >= 0);
           }
           fetch(set);
           if (++ki < n_own) step(wi);
@@ -1328,7 +1332,7 @@ cudaError_t ks_stream(const KeyScanParams& p, cudaStream_t st) {
   const long long most = (long long)p.S * p.Hkv * ((p.L + ks::BM - 1) / ks::BM);
   const int sms = ks_sms();
   const int grid = (int)(most < sms ? most : sms);
-  kern<<<grid, ks::THREADS, ly.total, st>>>(p, tma, t0, t1);
+  kern<<<grid, ks::kThreads<QUANT>, ly.total, st>>>(p, tma, t0, t1);
   return cudaGetLastError();
 }
 
