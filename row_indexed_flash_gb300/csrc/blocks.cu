@@ -33,6 +33,13 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+// A 16-byte load that stays where it is written: a thread's loads all go out
+// before the first is used (left to itself the compiler uses each at once).
+__device__ __forceinline__ uint4 load_in_order(const void* p) {
+  uint4 w;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+  return w;
+}
 __device__ __forceinline__ uint16_t round16(float x, bool up, bool bf16) {
   if (bf16) return __bfloat16_as_ushort(up ? __float2bfloat16_ru(x) : __float2bfloat16_rd(x));
   return __half_as_ushort(up ? __float2half_ru(x) : __float2half_rd(x));
@@ -89,7 +96,7 @@ __global__ void __launch_bounds__(kBndThreads) bounds_kernel(const BoundsParams 
 #pragma unroll
     for (int i = 0; i < kBndRows; ++i) {
       const int r = rg + i * nrg < fill ? rg + i * nrg : 0;
-      w[i] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * cpr * 16));
+      w[i] = load_in_order(src + (size_t)r * cpr * 16);
       if (QUANT) s16[i] = __ldg(sc + r);
     }
     if constexpr (QUANT) {
