@@ -238,7 +238,10 @@ fa_status fa_rows_prefill_heads(const fa_rows_args* a, void* ws, size_t ws_bytes
  * decay = 0 overwrites (acc is not read).  With S * Nq = 0 nothing is done.
  *   acc      [S, Hkv, L] fp32
  *   pools    every kind of fa_rows_args, D <= 256 with 16-byte multiples per
- *            (row, KV head); any mask kind; any Nq and Hq / Hkv
+ *            (row, KV head); any mask kind; any Nq and Hq / Hkv; L and Nq * Hq
+ *            up to 2^30.  D 64, 128 and 256 without a dense mask, with 16-byte
+ *            aligned q and at most 128 (D 256: 64) query heads per KV head,
+ *            take the tensor cores
  *   ws       256 bytes, zero-filled once (it holds the status word)
  * The order of the sums is fixed: equal calls give equal bits.
  */
@@ -394,7 +397,7 @@ fa_status fa_kv_block_bounds(const void* k, fa_dtype kv_dtype, const uint16_t* k
  *              when slice_seq is NULL (several slices of one sequence: prompt tiles).
  *              A slice whose slice_seq is outside 0 .. n_seq-1 scores minus infinity.
  *   seq_len    [S] int32: positions that slice s may see
- *   score      [S, Hkv, max_pages] fp32
+ *   score      [S, Hkv, max_pages] fp32; with S * Nq = 0 nothing is written
  *   ws         256 bytes, zero-filled once (it holds the status word)
  */
 fa_status fa_kv_block_scores(const void* q, fa_dtype q_dtype, int32_t S, int32_t Nq, int32_t Hq, int32_t Hkv, int32_t D,

@@ -309,13 +309,16 @@ def fa_rows_prefill(q, k, v, kv_rows, scale, **kw):
     return _attend("fa_rows_prefill", True, q, k, v, kv_rows, scale, **kw)
 
 
+_ATTEND_TENSORS = ("kv_len", "k_scale", "v_scale", "out", "lse", "workspace")
+
+
 def fa_rows_decode_heads(q, k, v, kv_rows, scale, **kw):
     """Decode over one list per (slice, KV head): kv_rows int32 [S, Hkv, L], kv_len int32 [S, Hkv].
 
     Keyword args as fa_rows_decode, without mask; n_valid_hint is the entries of
     all lists divided by Hkv.
     """
-    _same_device(q.device, k, v, kv_rows, kw.get("kv_len"))
+    _same_device(q.device, k, v, kv_rows, *(kw.get(x) for x in _ATTEND_TENSORS))
     with _on(q.device):
         return _attend("fa_rows_decode_heads", False, q, k, v, kv_rows, scale, head_lists=True, **kw)
 
@@ -323,7 +326,7 @@ def fa_rows_decode_heads(q, k, v, kv_rows, scale, **kw):
 def fa_rows_prefill_heads(q, k, v, kv_rows, scale, **kw):
     """Prefill over one list per (slice, KV head), as fa_rows_decode_heads; causal: each list
     ends with the slice's Nq newest positions."""
-    _same_device(q.device, k, v, kv_rows, kw.get("kv_len"))
+    _same_device(q.device, k, v, kv_rows, *(kw.get(x) for x in _ATTEND_TENSORS))
     with _on(q.device):
         return _attend("fa_rows_prefill_heads", True, q, k, v, kv_rows, scale, head_lists=True, **kw)
 
@@ -355,6 +358,8 @@ def _on(device):
 
 
 def _same_device(device, *tensors):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
     index = device.index
     for t in tensors:
         if t is not None and t.get_device() != index:

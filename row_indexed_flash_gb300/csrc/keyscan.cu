@@ -18,17 +18,25 @@
 //   8      MMA issue; allocates tensor memory
 //   9      queries of the next (slice, KV head), into one of two buffers: its
 //          rows and, for weights, lse in log2 units and the causal limits
-//   10 on  keys: two groups of four warps (eight for codes) on alternate tiles (one group's
-//          instructions per tile take longer than the tile's share of HBM
-//          time), two warps for each 64-row half; cp.async of the listed rows
-//          into the 128-byte-swizzled layout, or one TMA tile load per 64
-//          columns where the half is one contiguous pool run.  The copies
-//          arrive on the stage's barrier by themselves.
+//   10 on  keys: two groups of four warps (eight for codes) on alternate tiles
+//          (one group's instructions per tile take longer than the tile's share
+//          of HBM time), half of them for each 64-row half; cp.async of the
+//          listed rows into the 128-byte-swizzled layout, or one TMA tile load
+//          per 64 columns where the half is one contiguous pool run.  The
+//          copies arrive on the stage's barrier by themselves.
 // Scores take two stages per tile (kmax with max(q, 0), then kmin with
 // min(q, 0)), accumulated by the tensor core.  Codes of quantised pools are
 // copied to a ring in shared memory, widened exactly to Q's type by the lanes
 // that copied them, and the row's scale multiplies the product afterwards.
 // Every wait is bounded in time and reported through the workspace's status word.
+//
+// Measured, 4 slices x 16,384 listed rows of a shuffled pool, 8 KV heads, D 128,
+// four query vectors each (136 MB of keys and totals): 30 us, 4.6 TB/s; another
+// 16,384 rows per slice add 22 us, 6.3 TB/s (0.93 of the copy rate), so what
+// keeps the short call from it is about 6 us of start and end (a call of one
+// tile per CTA takes that).  INT8 33 us, INT4 32 us, E4M3 36 us: there the
+// widening holds it, not the bytes.  Scores of 32 sequences of 1k to 128k
+// tokens (58 MB of bounds) 21 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>

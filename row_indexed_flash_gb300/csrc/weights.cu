@@ -9,9 +9,10 @@
 // thread and its terms are added in one fixed order: no atomics, the same bits
 // every time.
 //
-// This file holds the CUDA-core kernel, for what the tensor-core kernels do
-// not take (dense masks, head dims other than 64, 128 and 256, unaligned Q):
-// a CTA stages 128 listed keys as fp32 (codes times scale: exact) in shared
+// This file holds the CUDA-core kernel, for what the tensor-core kernels
+// (keyscan.cu) do not take: dense masks, head dims other than 64, 128 and 256,
+// unaligned Q, very wide groups (4 x 16,384 rows, D 128, four query vectors:
+// 198 us here, 30 us there).  A CTA stages 128 listed keys as fp32 (codes times scale: exact) in shared
 // memory, one thread per key forms the logits of eight query vectors at a time
 // (broadcast reads of the staged queries) and adds their weights.  Rows are
 // padded by one word, so the 32 keys of a warp lie on 32 banks.
