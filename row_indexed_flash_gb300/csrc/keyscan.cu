@@ -821,10 +821,11 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
 //
 // A CTA owns up to NT tiles of 128 keys, so that each staged query tile is
 // used NT times; one warpgroup reduces each key tile (thread = key, as above)
-// while the tensor core is at the others.  The NBUF >= NT accumulators go round in
-// the order of the products (then the product before in the same accumulator
-// is no newer than the warpgroup's own last one, and its wait stays within
-// one phase of the barrier).  Measured for a 2,048-token chunk over 16,384
+// while the tensor core is at the others.  Each key tile has BPT accumulators of
+// its own.  Two warps issue the products, of alternate key tiles (weights) or
+// query tiles (scores): an issued product holds its warp until the tensor core
+// takes it, and the 300-odd clocks of one warp's waits and commits lie under
+// the other's products.  Measured for a 2,048-token chunk over 16,384
 // entries of 8 heads, D 128: NT 4 with 128 columns 230 us, NT 3 with a fourth
 // accumulator 247 us, NT 4 with five of 96 columns 272 us (a product costs the
 // issuing warp about the same whatever its columns), a polynomial for 3 of 8
@@ -841,18 +842,20 @@ struct Shape {
   static constexpr bool SC = MODE == SCAN_SCORES;
   static constexpr int NT = SC ? 1 : D == 256 ? 2 : 4;      // key tiles
   static constexpr int N = D == 256 ? 64 : 128;             // query vectors per tile
-  static constexpr int NBUF = 4;                            // accumulators
+  static constexpr int NBUF = 4, BPT = NBUF / NT;           // accumulators, and those of a key tile
   static constexpr int NK = SC ? 2 : 1;                     // stages per query tile
   static constexpr int NST = SC ? (D == 256 ? 2 : 4) : D == 64 ? 4 : 2;
   static constexpr int NL = 4;                              // query tiles whose lse are on chip
   static constexpr int ATOM = ks::BM * 128;
   static constexpr int KMAT = ks::BM * D * 2;         // one matrix of one key tile
   static constexpr int QST = N * D * 2;               // one query stage
-  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + 1, NQW = SC ? 8 : 1;
+  // Issuing warps.  Scores of D 256 have one: two would need a pair of stages each.
+  static constexpr int NMMA = SC && NST < 2 * NK ? 1 : 2;
+  static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + NMMA, NQW = SC ? 8 : 1;
   static constexpr int THREADS = (W_Q + NQW) * 32;
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
-  static constexpr int NBAR = 1 + 2 * NST + 2 * NBUF + 1 + 2 * NL;
+  static constexpr int NBAR = 2 + 2 * NST + 2 * NBUF + NMMA + 2 * NL;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NL][N] lse, [NL][N] limits, [NL] flags
   static constexpr int OFF_IDX = OFF_L + (SC ? 0 : NL * N * 8 + NL * 4);
@@ -875,19 +878,20 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     keyscan_prompt_kernel(const KeyScanParams p, const PromptPlan pl, const __grid_constant__ CUtensorMap tq) {
   using Sh = kp::Shape<D, MODE>;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
-  constexpr int NT = Sh::NT, N = Sh::N, NBUF = Sh::NBUF, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
+  constexpr int NT = Sh::NT, N = Sh::N, NBUF = Sh::NBUF, BPT = Sh::BPT, NMMA = Sh::NMMA, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
   constexpr int BM = ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
   // aligned by an offset, so that the compiler still knows the pointer for a shared one (plain, not generic, loads)
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* key_full = reinterpret_cast<uint64_t*>(sm + Sh::OFF_BAR);
-  uint64_t* q_full = key_full + 1;
+  uint64_t* key_seen = key_full + 1;     // both issuing warps have seen key_full's last phase
+  uint64_t* q_full = key_seen + 1;
   uint64_t* q_empty = q_full + NST;
   uint64_t* s_full = q_empty + NST;
   uint64_t* s_empty = s_full + NBUF;
   uint64_t* drain = s_empty + NBUF;
-  uint64_t* l_full = drain + 1;          // [NL] lse, limits and flag of a query tile
+  uint64_t* l_full = drain + NMMA;       // [NL] lse, limits and flag of a query tile
   uint64_t* l_empty = l_full + NL;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + Sh::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::OFF_MISC + 4);
@@ -919,9 +923,10 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
 
   if (tid == 0) {
     mbar_init(key_full, Sh::NEPI * 32);
+    mbar_init(key_seen, NMMA);
     for (int i = 0; i < NST; ++i) {
       mbar_init(q_full + i, MODE == SCAN_SCORES ? Sh::NQW : 1);
-      mbar_init(q_empty + i, 1);
+      mbar_init(q_empty + i, MODE == SCAN_SCORES ? 1 : NMMA);
     }
     for (int i = 0; i < NL; ++i) {
       mbar_init(l_full + i, 1);
@@ -931,7 +936,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       mbar_init(s_full + i, 1);
       mbar_init(s_empty + i, 4);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < NMMA; ++i) mbar_init(drain + i, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -960,9 +965,9 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     const int j = kt < tile_end - tile0 ? j0 + kt * BM + e : p.L;   // past every entry where the batch has no such tile
     int* my_idx = idx + kt * BM;
     unsigned char* kdst = sm + kt * NK * Sh::KMAT;
-    int loaded = -1, row = -1;
+    int loaded = -1, loads = 0, row = -1;
     float cs = p.c;
-    int seq = 0, lround = 0;                               // products of the CTA and lse slots so far
+    int round = 0, lround = 0;                             // query tiles and lse slots so far
     bool ok = true;
     for (int s = s_lo; ok && s < s_hi; ++s) {
       const int n = ks_entries<MODE>(p, s);
@@ -975,8 +980,11 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       const int list = list_of_slice(s);
       if (list != loaded) {
         // This warpgroup's key tile: its products of earlier slices have all
-        // been read, so nothing else uses the tile.  For scores every page of
-        // the table is staged, since later slices may see more of them.
+        // been read, so nothing else uses the tile; but an issuing warp that had
+        // none of them may not have looked at key_full since.  For scores every
+        // page of the table is staged, since later slices may see more of them.
+        if (loads > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(key_seen, (loads - 1) & 1, abort_flag, wait_ns)))) break;
+        ++loads;
         loaded = list;
         row = j < (MODE == SCAN_SCORES ? p.L : n) ? __ldg(p.rows + (size_t)list * p.L + j) : -1;
         row = row >= 0 && (long long)row < p.R ? row : -1;
@@ -1025,15 +1033,14 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (lround / NL) & 1, abort_flag, wait_ns)))) break;
           ++lround;
         }
-        const int mine_seq = seq + kt;
-        seq += kn;
+        const int b = kt * BPT + round % BPT, phase = (round / BPT) & 1;
+        ++round;
         if (kt >= kn) {   // no such key tile
           __syncwarp();
           if (MODE == SCAN_WEIGHTS && lane == 0) mbar_arrive(l_empty + sl);
           continue;
         }
-        const int b = mine_seq % NBUF;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, (mine_seq / NBUF) & 1, abort_flag, wait_ns)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, phase, abort_flag, wait_ns)))) break;
         tc_fence_after();
         const uint32_t at = tbase + lanes + b * N;
         const int m = p.NV - t * N;      // scores: real columns of the tile
@@ -1116,14 +1123,30 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         out[j] = -INF;
       }
     }
-  } else if (warp == Sh::W_MMA) {
+  } else if (warp < Sh::W_Q) {
     // ------------------------------------------------------------ MMA issue
+    const int mw = warp - Sh::W_MMA;
     const uint32_t id = make_idesc_f16(BM, N, bf16, false);
     const uint64_t dK = sdesc_sw128(smem_u32(sm), 16, 1024);
     const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
     bool ok = true;
-    int loaded = -1, loads = 0;
-    Ring qr, sr;
+    int loaded = -1, loads = 0, round = 0;
+    // The products of stage st (part m of a query tile) with key tile kt
+    auto product = [&](int kt, int m, int st) -> bool {
+      const int b = kt * BPT + round % BPT;
+      if (m == 0 && !ks_poll(s_empty + b, ((round / BPT) & 1) ^ 1, abort_flag, wait_ns)) return false;
+      tc_fence_after();
+      const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT), q = sdesc_at(dQ, st * Sh::QST);
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          mma_ss(tbase + b * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
+                 sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
+        if (m == NK - 1) tc_commit(s_full + b);
+      }
+      __syncwarp();
+      return true;
+    };
     for (int s = s_lo; ok && s < s_hi; ++s) {
       const int n = ks_entries<MODE>(p, s);
       const int T = nt - first_tile(n);
@@ -1134,32 +1157,21 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         loaded = list;
         ok = ks_poll(key_full, loads & 1, abort_flag, wait_ns);
         ++loads;
+        if (ok && lane == 0) mbar_arrive(key_seen);
         fence_proxy_async_smem();   // the keys' cp.async copies arrived by themselves
       }
-      for (int t = 0; ok && t < T; ++t) {
+      for (int t = 0; ok && t < T; ++t, ++round) {
+        if (MODE == SCAN_SCORES && NMMA == 2 && (round & 1) != mw) continue;   // the other warp's query tile, and its stages
 #pragma unroll
         for (int m = 0; m < NK; ++m) {
-          const int st = qr.st;
-          ok = ok && ks_poll(q_full + st, qr.ph, abort_flag, wait_ns);
-          if (!ok) break;
-          qr.next(NST);
-          const uint64_t q = sdesc_at(dQ, st * Sh::QST);
+          const int use = round * NK + m, st = use % NST;
+          if (!(ok = ks_poll(q_full + st, (use / NST) & 1, abort_flag, wait_ns))) break;
+          if (MODE == SCAN_SCORES) {
+            ok = product(0, m, st);
+          } else {
 #pragma unroll
-          for (int kt = 0; kt < NT; ++kt) {
-            if (kt >= kn || !ok) continue;
-            if (m == 0) ok = ks_poll(s_empty + sr.st, sr.ph ^ 1u, abort_flag, wait_ns);
-            if (!ok) continue;
-            tc_fence_after();
-            const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT);
-            if (elect_one()) {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                mma_ss(tbase + sr.st * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
-                       sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
-              if (m == NK - 1) tc_commit(s_full + sr.st);
-            }
-            __syncwarp();
-            if (m == NK - 1) sr.next(NBUF);
+            for (int kt = 0; kt < NT; kt += NMMA)
+              if (ok && kt + mw < kn) ok = product(kt + mw, m, st);
           }
           if (!ok) break;
           if (elect_one()) tc_commit(q_empty + st);
@@ -1168,8 +1180,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       }
     }
     if (elect_one()) {
-      tc_commit(drain);
-      ks_wait_drain(drain, 0);
+      tc_commit(drain + mw);
+      ks_wait_drain(drain + mw, 0);
     }
     __syncwarp();
   } else if (MODE == SCAN_WEIGHTS) {

@@ -332,3 +332,14 @@ def test_block_sparse_prompt_chain_in_a_graph():
                                          query_rows=pick, n_query=Nq, kv_format="bf16")
     assert_parity(out[:, pick], ref, "prompt chain")
     assert_lse(lse[:, pick], lref)
+
+
+def test_scores_of_many_slices_of_alternating_sequences():
+    # a CTA walks several slices and stages the bounds again at every change of sequence; one query
+    # tile per slice, so the issuing warps take turns
+    for Nq, S in ((33, 40), (70, 33), (17, 60)):
+        g = synth.rng(150 + Nq)
+        seq = g.integers(0, 3, size=S)
+        lens = g.integers(0, 64 * 130, size=S)
+        lens[::9] = 0
+        check_scores(*score_case(151 + Nq, S=S, Nq=Nq, Hq=8, Hkv=2, D=128, P=140, NB=130, lens=lens, slice_seq=seq, n_seq=3))
