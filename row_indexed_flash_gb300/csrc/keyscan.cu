@@ -826,10 +826,12 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
 // query tiles (scores): an issued product holds its warp until the tensor core
 // takes it, and the 300-odd clocks of one warp's waits and commits lie under
 // the other's products.  Measured for a 2,048-token chunk over 16,384
-// entries of 8 heads, D 128: NT 4 with 128 columns 230 us, NT 3 with a fourth
-// accumulator 247 us, NT 4 with five of 96 columns 272 us (a product costs the
-// issuing warp about the same whatever its columns), a polynomial for 3 of 8
-// exponentials 345 us.
+// entries of 8 heads, D 128: NT 4 with 128 columns and one accumulator per key
+// tile 229 us (1.13 PFLOP/s; the tensor core and the exponentials are each busy
+// 53 % of the time); 64 columns and two accumulators 253 us; NT 3 with a
+// fourth accumulator going round 247 us; 96 columns with five going round 272 us (a
+// product costs about the same whatever its columns); a polynomial for 3 of
+// 8 exponentials 345 us (the special-function units give 32 a clock and SM here).
 // Scores (two stages per query tile, for max(q, 0) and min(q, 0)) keep both
 // bounds of one key tile; a CTA walks several slices, and stages the bounds
 // again only where the slice is of another sequence.
