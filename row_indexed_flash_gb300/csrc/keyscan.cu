@@ -4,8 +4,8 @@
 //   scores   score[s, g, b] = max_v <max(q_v, 0), kmax[page_b, g]> + <min(q_v, 0), kmin[page_b, g]>
 //
 // Bound by the bytes of the keys: each is read once.  The keys of a tile are
-// the 128 rows of the MMA's M dimension and the at most 64 query vectors of
-// the KV head its N columns, so a key's products lie in one tensor-memory lane
+// the 128 rows of the MMA's M dimension and the few query vectors of the KV
+// head its N columns, so a key's products lie in one tensor-memory lane
 // and one thread reduces them in registers, in a fixed order, with nothing
 // exchanged between threads and one fp32 written per key.
 //
@@ -59,7 +59,7 @@ template <bool QUANT>
 constexpr int kThreads = (W_KEY + kKeyWarps<QUANT>) * 32;
 constexpr int NBUF = 4;                    // accumulators
 constexpr int MAXST = 8;                  // stages
-constexpr int MAXN = kScanStreamVec;
+constexpr int MAXN = 128;                  // query vectors, at most (see kStreamVec)
 constexpr int PRE = 3;                     // own tiles ahead that a key warp loads list entries
 // Groups of key warps on alternate tiles: two, but one for the codes of D 256
 // (two groups' code rings do not fit beside their operand stage) and for its
@@ -69,6 +69,12 @@ constexpr int PRE = 3;                     // own tiles ahead that a key warp lo
 template <int D, int NK, bool QUANT>
 constexpr int kGroups = D > 128 && (QUANT || NK == 2) ? 1 : 2;
 constexpr int SMEM_MAX = 225 * 1024;
+// Query vectors that the streaming form takes; more go to the prompt form.  Four
+// slices of 16,384 entries, D 128, bf16, 8 heads: 64 vectors 33 us here and 60
+// there, 128 vectors 42 us here and 59 there.  With two D-wide query parts
+// (scores), codes or D 256 only 64 vectors leave room for the stages.
+template <int D, int NK, bool QUANT>
+constexpr int kStreamVec = NK == 1 && !QUANT && D <= 128 ? 128 : 64;
 }  // namespace ks
 
 namespace {
@@ -81,7 +87,7 @@ enum { SCAN_WEIGHTS = 0, SCAN_SCORES = 1 };
 template <int D, int KIND>
 __host__ __device__ constexpr int ks_ahead() {
   const int code = ks::kGroups<D, 1, true> * ks::BM * kv_row_bytes<KIND>(D);
-  const int room = ks::SMEM_MAX - 3072 - 2 * ks::MAXN * D * 2 - (D <= 128 ? 2 : 1) * ks::BM * D * 2;
+  const int room = ks::SMEM_MAX - 4096 - 2 * ks::kStreamVec<D, 1, true> * D * 2 - (D <= 128 ? 2 : 1) * ks::BM * D * 2;
   const int n = room / code - 1;
   return n > ks::PRE ? ks::PRE : n;
 }
@@ -103,7 +109,7 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   l.code = QUANT ? ks::BM * kv_row_bytes<KIND>(D) : 0;
   l.off_q = 0;
   l.off_k = (2 * l.qb_bytes + 1023) / 1024 * 1024;
-  const int room = ks::SMEM_MAX - 1024 - l.off_k - 2048;
+  const int room = ks::SMEM_MAX - 1024 - l.off_k - 3072;
   if (QUANT) {
     // the code ring, operand stages with what is left (two at least; one for D 256)
     l.ncs = ks::kGroups<D, 1, true> * (ks_ahead<D, KIND>() + 1);
@@ -821,8 +827,8 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
 //
 // A CTA owns up to NT tiles of 128 keys, so that each staged query tile is
 // used NT times; one warpgroup reduces each key tile (thread = key, as above)
-// while the tensor core is at the others.  Each key tile has BPT accumulators of
-// its own.  Two warps issue the products, of alternate key tiles (weights) or
+// while the tensor core is at the others.  Each key tile has its own of the four
+// accumulators.  Two warps issue the products, of alternate key tiles (weights) or
 // query tiles (scores): an issued product holds its warp until the tensor core
 // takes it, and the 300-odd clocks of one warp's waits and commits lie under
 // the other's products.  Measured for a 2,048-token chunk over 16,384
@@ -844,7 +850,7 @@ struct Shape {
   static constexpr bool SC = MODE == SCAN_SCORES;
   static constexpr int NT = SC ? 1 : D == 256 ? 2 : 4;      // key tiles
   static constexpr int N = D == 256 ? 64 : 128;             // query vectors per tile
-  static constexpr int NBUF = 4, BPT = NBUF / NT;           // accumulators, and those of a key tile
+  static constexpr int NBUF = 4;                            // accumulators
   static constexpr int NK = SC ? 2 : 1;                     // stages per query tile
   static constexpr int NST = SC ? (D == 256 ? 2 : 4) : D == 64 ? 4 : 2;
   static constexpr int NL = 4;                              // query tiles whose lse are on chip
@@ -864,7 +870,7 @@ struct Shape {
   static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
   static constexpr int SMEM = USED + 1024;
   static constexpr uint32_t COLS = NBUF * N;
-  static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0, "tensor memory");
+  static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0 && NBUF >= NT && NBUF == 4, "tensor memory");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 }  // namespace kp
@@ -880,7 +886,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     keyscan_prompt_kernel(const KeyScanParams p, const PromptPlan pl, const __grid_constant__ CUtensorMap tq) {
   using Sh = kp::Shape<D, MODE>;
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
-  constexpr int NT = Sh::NT, N = Sh::N, NBUF = Sh::NBUF, BPT = Sh::BPT, NMMA = Sh::NMMA, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
+  constexpr int NT = Sh::NT, N = Sh::N, NBUF = Sh::NBUF, NMMA = Sh::NMMA, NK = Sh::NK, NST = Sh::NST, NL = Sh::NL, KT = D / 64;
   constexpr int BM = ks::BM;
   const float INF = __int_as_float(0x7f800000);
   extern __shared__ unsigned char smem_raw[];
@@ -920,6 +926,11 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     if (j0 >= n) return nt;
     return MODE == SCAN_WEIGHTS && p.causal ? min(nt, max(0, j0 - (n - p.Nq)) / pl.PT) : 0;
   };
+  // Accumulators of each key tile, as a power of two: all four for one, two each
+  // for two, else one.  (By the batch's own number of tiles instead of the most
+  // it can have: 236 us for 229 in the case above.)
+  constexpr int bpt = NT == 1 ? 2 : NT == 2 ? 1 : 0;
+  auto buffer = [&](int kt, int round) { return (kt << bpt) + (round & ((1 << bpt) - 1)); };
   auto key_tiles = [&](int n) { return min(tile_end - tile0, (n - j0 + BM - 1) / BM); };   // for n > j0
   if (MODE == SCAN_WEIGHTS && j0 >= ks_entries<MODE>(p, s_lo)) return;
 
@@ -994,16 +1005,26 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         named_barrier(1 + kt, 128);
         if constexpr (QUANT) {
           constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, W = KvChunk<KIND>::N / 8;
-#pragma unroll 4
-          for (int f = e; f < BM * CPR; f += BM) {
-            const int k = f / CPR, c = f % CPR, r = my_idx[k];
-            uint4 o[W];
-            const uint4 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k[0]) + ((size_t)max(r, 0) * p.Hkv + g) * CB) + c);
-            widen_chunk<KIND>(r >= 0 ? y : make_uint4(0u, 0u, 0u, 0u), bf16, o);
+          constexpr int B = CPR < 8 ? CPR : 8;   // chunks per thread and step, all loaded before any is widened
+          const char* src = static_cast<const char*>(p.k[0]) + (size_t)g * CB;
+          const size_t pitch = (size_t)p.Hkv * CB;
+          for (int f0 = e; f0 < BM * CPR; f0 += B * BM) {
+            uint4 y[B];
 #pragma unroll
-            for (int x = 0; x < W; ++x) {
-              const int cc = c * W + x;
-              *reinterpret_cast<uint4*>(kdst + (cc >> 3) * Sh::ATOM + k * 128 + (((cc & 7) ^ (k & 7)) << 4)) = o[x];
+            for (int u = 0; u < B; ++u) {
+              const int f = f0 + u * BM, r = my_idx[f / CPR];
+              y[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + r * pitch) + f % CPR) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+              const int f = f0 + u * BM, k = f / CPR, c = f % CPR;
+              uint4 o[W];
+              widen_chunk<KIND>(y[u], bf16, o);
+#pragma unroll
+              for (int x = 0; x < W; ++x) {
+                const int cc = c * W + x;
+                *reinterpret_cast<uint4*>(kdst + (cc >> 3) * Sh::ATOM + k * 128 + (((cc & 7) ^ (k & 7)) << 4)) = o[x];
+              }
             }
           }
           fence_proxy_async_smem();
@@ -1035,7 +1056,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(l_full + sl, (lround / NL) & 1, abort_flag, wait_ns)))) break;
           ++lround;
         }
-        const int b = kt * BPT + round % BPT, phase = (round / BPT) & 1;
+        const int b = buffer(kt, round), phase = (round >> bpt) & 1;
         ++round;
         if (kt >= kn) {   // no such key tile
           __syncwarp();
@@ -1135,8 +1156,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     int loaded = -1, loads = 0, round = 0;
     // The products of stage st (part m of a query tile) with key tile kt
     auto product = [&](int kt, int m, int st) -> bool {
-      const int b = kt * BPT + round % BPT;
-      if (m == 0 && !ks_poll(s_empty + b, ((round / BPT) & 1) ^ 1, abort_flag, wait_ns)) return false;
+      const int b = buffer(kt, round);
+      if (m == 0 && !ks_poll(s_empty + b, ((round >> bpt) & 1) ^ 1, abort_flag, wait_ns)) return false;
       tc_fence_after();
       const uint64_t a = sdesc_at(dK, (kt * NK + m) * Sh::KMAT), q = sdesc_at(dQ, st * Sh::QST);
       if (elect_one()) {
@@ -1416,7 +1437,9 @@ cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
 
 template <int D, int MODE, int KIND>
 cudaError_t ks_launch(const KeyScanParams& p, cudaStream_t st) {
-  return p.NV <= kScanStreamVec ? ks_stream<D, MODE, KIND>(p, st) : ks_prompt<D, MODE, KIND>(p, st);
+  constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
+  constexpr int most = ks::kStreamVec<D, MODE == SCAN_SCORES ? 2 : 1, QUANT>;
+  return p.NV <= most ? ks_stream<D, MODE, KIND>(p, st) : ks_prompt<D, MODE, KIND>(p, st);
 }
 
 template <int KIND>

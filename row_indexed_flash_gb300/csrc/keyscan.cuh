@@ -27,9 +27,6 @@ struct KeyScanParams {
   unsigned long long wait_ns;
 };
 
-// Query vectors per KV head that the streaming form keeps on chip.
-constexpr int kScanStreamVec = 64;
-
 bool keyscan_supported(int D, int G);   // weights: the head dims and groups taken
 cudaError_t keyscan_weights(const KeyScanParams& p, int D, int kind, cudaStream_t st);
 cudaError_t keyscan_scores(const KeyScanParams& p, int D, cudaStream_t st);
