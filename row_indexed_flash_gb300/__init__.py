@@ -190,7 +190,7 @@ _workspaces = {}
 
 def _default_ws(device, stream_handle, is_prefill: bool) -> _Workspace:
     """The binding's own workspace for calls without one: one per (device, stream, decode or prefill)."""
-    key = (str(device), stream_handle, bool(is_prefill))
+    key = (device, stream_handle, bool(is_prefill))
     if key not in _workspaces:
         _workspaces[key] = _Workspace()
     return _workspaces[key]
@@ -366,6 +366,24 @@ def _same_device(device, *tensors):
             raise ValueError(f"tensors must share one device ({t.device} and {device})")
 
 
+def _ptrs(device, *tensors):
+    """Pointers of tensors (None: None) that must be contiguous and on ``device``."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    index = device.index
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != index:
+            raise ValueError(f"tensors must share one device ({t.device} and {device})")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
 def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, kv_len=None, mask=None, causal=False,
                     k_scale=None, workspace=None, stream=None, check_status=False) -> torch.Tensor:
     """acc [S, Hkv, L] += the softmax weight each list entry received from the attention call that
@@ -387,20 +405,20 @@ def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, 
         acc = torch.zeros((S, Hkv, L), dtype=torch.float32, device=q.device)
     elif acc.dtype != torch.float32 or acc.shape != (S, Hkv, L):
         raise ValueError("acc must be float32 [S, Hkv, L]")
-    _same_device(q.device, k, kv_rows, lse, acc, kv_len, mask, k_scale, workspace)
+    dev = q.device
     a = fa_rows_args()
-    a.q, a.q_dtype = _ptr(q), _DT[q.dtype]
-    a.k, a.kv_dtype, a.k_scale = _ptr(k), _DT[k.dtype], _ptr(k_scale)
+    a.q, a.k, a.k_scale, a.kv_rows, a.kv_len, a.mask, plse, pacc, _ = _ptrs(
+        dev, q, k, k_scale, kv_rows, kv_len, mask, lse, acc, workspace)
+    a.q_dtype, a.kv_dtype = _DT[q.dtype], _DT[k.dtype]
     a.n_pool_rows = R
-    a.kv_rows, a.list_len, a.kv_len = _ptr(kv_rows), L, _ptr(kv_len)
+    a.list_len = L
     a.mask_kind = FA_MASK_DENSE if mask is not None else FA_MASK_CAUSAL if causal else FA_MASK_NONE
-    a.mask = _ptr(mask)
     a.scale = float(scale)
     a.S, a.Nq, a.Hq, a.Hkv, a.D = S, Nq, Hq, Hkv, D
-    with _on(q.device):
-        sh = _stream(stream, q.device)
-        wptr, wbytes, wtensor = _status_ws(workspace, q.device, sh)
-        _check(lib().fa_rows_weights(ctypes.byref(a), _ptr(lse), float(decay), _ptr(acc), wptr, wbytes, sh))
+    with _on(dev):
+        sh = _stream(stream, dev)
+        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh)
+        _check(lib().fa_rows_weights(ctypes.byref(a), plse, float(decay), pacc, wptr, wbytes, sh))
     if check_status:
         _raise_expired("fa_rows_weights", wtensor, stream)
     return acc
@@ -435,10 +453,9 @@ def fa_kv_evict(acc, kv_rows, kv_len, sinks: int, recent: int, k: int, *, out_le
     acc_out = dest(acc_out, (S, Hkv, n), torch.float32, "acc_out")
     kept = dest(kept, (S, n), torch.int32, "kept")
     freed = dest(freed, (S, L), torch.int32, "freed")
-    _same_device(dev, kv_rows, kv_len, rows_out, len_out, acc_out, kept, freed)
+    pa, pr, pl, po, pro, plo, pk, pf = _ptrs(dev, acc, kv_rows, kv_len, acc_out, rows_out, len_out, kept, freed)
     with _on(dev):
-        _check(lib().fa_kv_evict(_ptr(acc), _ptr(kv_rows), _ptr(kv_len), S, Hkv, L, int(sinks), int(recent), int(k),
-                                 _ptr(acc_out), _ptr(rows_out), _ptr(len_out), n, _ptr(kept), _ptr(freed),
+        _check(lib().fa_kv_evict(pa, pr, pl, S, Hkv, L, int(sinks), int(recent), int(k), po, pro, plo, n, pk, pf,
                                  _stream(stream, dev)))
     return rows_out, len_out, acc_out, kept, freed
 
@@ -456,11 +473,11 @@ def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None)
     if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
         if k_scale is None:
             raise ValueError("a quantised pool needs k_scale")
-    _same_device(k.device, pages, fill, kmin, kmax, k_scale)
-    with _on(k.device):
-        _check(lib().fa_kv_block_bounds(_ptr(k), _DT[k.dtype], _ptr(k_scale), R, Hkv, D, _ptr(pages), _ptr(fill),
-                                        pages.shape[0], _ptr(kmin), _ptr(kmax), _DT[kmin.dtype],
-                                        _stream(stream, k.device)))
+    dev = k.device
+    pk, ps, pp, pf, plo, phi = _ptrs(dev, k, k_scale, pages, fill, kmin, kmax)
+    with _on(dev):
+        _check(lib().fa_kv_block_bounds(pk, _DT[k.dtype], ps, R, Hkv, D, pp, pf, pages.shape[0], plo, phi,
+                                        _DT[kmin.dtype], _stream(stream, dev)))
     return kmin, kmax
 
 
@@ -487,13 +504,13 @@ def fa_kv_block_scores(q, kmin, kmax, page_table, seq_len, *, slice_seq=None, ou
         out = torch.empty((S, Hkv, max_pages), dtype=torch.float32, device=q.device)
     elif out.dtype != torch.float32 or out.shape != (S, Hkv, max_pages):
         raise ValueError("out must be float32 [S, Hkv, max_pages]")
-    _same_device(q.device, kmin, kmax, page_table, seq_len, slice_seq, out, workspace)
-    with _on(q.device):
-        sh = _stream(stream, q.device)
-        wptr, wbytes, wtensor = _status_ws(workspace, q.device, sh)
-        _check(lib().fa_kv_block_scores(_ptr(q), _DT[q.dtype], S, Nq, Hq, Hkv, D, _ptr(kmin), _ptr(kmax), P,
-                                        _ptr(page_table), n_seq, max_pages, _ptr(seq_len), _ptr(slice_seq), _ptr(out),
-                                        wptr, wbytes, sh))
+    dev = q.device
+    pq, plo, phi, pt, pn, pseq, po, _ = _ptrs(dev, q, kmin, kmax, page_table, seq_len, slice_seq, out, workspace)
+    with _on(dev):
+        sh = _stream(stream, dev)
+        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh)
+        _check(lib().fa_kv_block_scores(pq, _DT[q.dtype], S, Nq, Hq, Hkv, D, plo, phi, P, pt, n_seq, max_pages, pn,
+                                        pseq, po, wptr, wbytes, sh))
     if check_status:
         _raise_expired("fa_kv_block_scores", wtensor, stream)
     return out
@@ -518,11 +535,11 @@ def fa_kv_block_rows(score, page_table, seq_len, sink_blocks: int, recent_blocks
         out_len = torch.empty((S, Hkv), dtype=torch.int32, device=score.device)
     elif out_len.dtype != torch.int32 or out_len.shape != (S, Hkv):
         raise ValueError("out_len must be int32 [S, Hkv]")
-    _same_device(score.device, page_table, seq_len, slice_seq, out, out_len)
-    with _on(score.device):
-        _check(lib().fa_kv_block_rows(_ptr(score), _ptr(page_table), page_table.shape[0], max_pages, _ptr(seq_len),
-                                      _ptr(slice_seq), S, Hkv, int(sink_blocks), int(recent_blocks), int(k), _ptr(out),
-                                      _ptr(out_len), L, _stream(stream, score.device)))
+    dev = score.device
+    ps, pt, pn, pseq, po, pol = _ptrs(dev, score, page_table, seq_len, slice_seq, out, out_len)
+    with _on(dev):
+        _check(lib().fa_kv_block_rows(ps, pt, page_table.shape[0], max_pages, pn, pseq, S, Hkv, int(sink_blocks),
+                                      int(recent_blocks), int(k), po, pol, L, _stream(stream, dev)))
     return out, out_len
 
 
