@@ -405,6 +405,7 @@ def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, 
         acc = torch.zeros((S, Hkv, L), dtype=torch.float32, device=q.device)
     elif acc.dtype != torch.float32 or acc.shape != (S, Hkv, L):
         raise ValueError("acc must be float32 [S, Hkv, L]")
+    _check_scale(k, k_scale)
     dev = q.device
     a = fa_rows_args()
     a.q, a.k, a.k_scale, a.kv_rows, a.kv_len, a.mask, plse, pacc, _ = _ptrs(
@@ -470,15 +471,21 @@ def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None)
     for t, name in ((pages, "pages"), (fill, "fill")):
         if t is not None and (t.dtype != torch.int32 or t.shape != pages.shape or t.dim() != 1):
             raise ValueError(f"{name} must be int32 [n_pages]")
-    if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
-        if k_scale is None:
-            raise ValueError("a quantised pool needs k_scale")
+    _check_scale(k, k_scale)
     dev = k.device
     pk, ps, pp, pf, plo, phi = _ptrs(dev, k, k_scale, pages, fill, kmin, kmax)
     with _on(dev):
         _check(lib().fa_kv_block_bounds(pk, _DT[k.dtype], ps, R, Hkv, D, pp, pf, pages.shape[0], plo, phi,
                                         _DT[kmin.dtype], _stream(stream, dev)))
     return kmin, kmax
+
+
+def _check_scale(k, k_scale):
+    if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+        if k_scale is None:
+            raise ValueError("a quantised pool needs k_scale")
+        if k_scale.element_size() != 2 or k_scale.numel() != k.shape[0] * k.shape[1]:
+            raise ValueError("k_scale must be fp16 [R/64, Hkv, 64]")
 
 
 def _check_pages(S, page_table, seq_len, slice_seq):

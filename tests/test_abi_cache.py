@@ -96,3 +96,15 @@ def test_binding_checks_shapes_before_pointers():
         far.fa_kv_block_scores(q, torch.zeros((1, 2, 64)), torch.zeros((1, 2, 64)), rows, torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         far.fa_kv_block_rows(torch.zeros((1, 2, 9)), rows, torch.zeros(1, dtype=torch.int32), 1, 1, 1)
+
+
+def test_binding_refuses_scales_of_another_pool():
+    q = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16)
+    k = torch.zeros((128, 2, 64), dtype=torch.int8)
+    rows = torch.zeros((1, 8), dtype=torch.int32)
+    bound = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    for ks in (None, torch.zeros((1, 2, 64), dtype=torch.float16), torch.zeros((2, 2, 64))):
+        with pytest.raises(ValueError, match="k_scale"):
+            far.fa_rows_weights(q, k, rows, 1.0, torch.zeros((1, 1, 4)), k_scale=ks)
+        with pytest.raises(ValueError, match="k_scale"):
+            far.fa_kv_block_bounds(k, rows[0], None, bound, bound.clone(), k_scale=ks)
