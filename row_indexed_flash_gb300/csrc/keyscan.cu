@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
       if (j < x.n) {
         const int list = MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + x.s) : x.s;
         a.row = __ldg(p.rows + (size_t)list * p.L + j);
-        if (MODE == SCAN_WEIGHTS && p.decay != 0.f) a.old = __ldg(p.out + ((size_t)x.s * p.Hkv + x.g) * p.L + j);
+        if (MODE == SCAN_WEIGHTS && p.decay != 0.f) a.old = __ldcg(p.out + ((size_t)x.s * p.Hkv + x.g) * p.L + j);
       }
     };
     auto live = [&](const Key& a) { return a.row >= 0 && (long long)a.row < p.R; };
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         }
       }
       float old = 0.f;
-      if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldg(out + j);
+      if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldcg(out + j);
       float total = MODE == SCAN_SCORES ? -INF : 0.f;
       const int kn = T > 0 ? key_tiles(n) : 0;
       for (int t = 0; t < T; ++t) {
