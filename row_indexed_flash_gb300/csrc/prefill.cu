@@ -731,6 +731,13 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
   if (threadIdx.x == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
 }
 
+// CTAs of the scan per SM: two, which stay and load the next tile's entries while
+// they read the rows of one.  (128 lists of 4,096 entries of one head, 134 MB out
+// of L2, prefill included: two 192 us, three 194, sixteen 196; a CTA for every
+// two tiles without that 198, and 201 with a comparison of two instructions a
+// value and an atomic a warp.)
+constexpr int kScanPerSm = 2;
+
 // Before a bf16 launch, per 128-entry KV tile of every list (a warp for each 32
 // of its entries: a warp for each tile left most SMs with three warps to wait
 // for memory with): is any listed V value finite and of magnitude 65536 or
@@ -743,66 +750,105 @@ template <bool HEADS>
 __global__ void __launch_bounds__(256) prefill_v_scan_kernel(const uint4* v, const int32_t* kv_rows,
                                                              const int32_t* kv_len, int nl, int L, long long R,
                                                              int row_chunks, int heads, int tma_kv, unsigned int* words) {
-  const int lane = threadIdx.x & 31;
+  __shared__ unsigned int sums[3];   // this CTA's share of the three words
+  if (threadIdx.x < 3) sums[threadIdx.x] = 0u;
+  __syncthreads();
+  // a CTA's eight warps take the quarters of two tiles, then step on by grid * 2 tiles
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
   const int tiles_per = (L + pf::BN - 1) / pf::BN;
-  const long long nw = (long long)gridDim.x * (blockDim.x >> 5);
+  const long long all = (long long)nl * tiles_per, first = 2ll * blockIdx.x + (warp >> 2), step = 2ll * gridDim.x;
+  const int ds = (int)(step / tiles_per), dt = (int)(step % tiles_per);
   uint32_t bad = 0;
   unsigned gathered = 0, tiles = 0;
   auto examine = [&](const uint4& w) {
     const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
     #pragma unroll
     for (int q = 0; q < 4; ++q) {
+      // 15-bit magnitudes, two a word: bit 15 of a + 0x3880 is a >= 0x4780 (65536),
+      // of a + 0x0080 a >= 0x7f80 (infinite or NaN); no sum carries into the next
       const uint32_t a = wv[q] & 0x7fff7fffu;
-      bad |= __vcmpgeu2(a, 0x47804780u) & __vcmpltu2(a, 0x7f807f80u);
+      bad |= (a + 0x38803880u) & ~(a + 0x00800080u);
     }
   };
-  for (long long e = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); e < 4ll * nl * tiles_per; e += nw) {
-    const int quarter = (int)(e & 3);
-    const int s = (int)((e >> 2) / tiles_per), j0 = (int)((e >> 2) % tiles_per) * pf::BN;
-    const int n_s = kv_len ? min(max(__ldg(kv_len + s), 0), L) : L;
-    if (j0 >= n_s) continue;
-    const int32_t* rows = kv_rows + (size_t)s * L + j0;
-    auto entry = [&](int pos) {
-      const int x = j0 + pos < n_s ? __ldg(rows + pos) : -1;
-      return (x < 0 || (long long)x >= R) ? -1 : x;
-    };
-    const int own = entry(quarter * 32 + lane);
-    if (quarter == 0) {
-      const int r[4] = {own, entry(lane + 32), entry(lane + 64), entry(lane + 96)};
-      int r0, r1;
-      ++tiles;
-      if (!(half_runs(r, lane, r0, r1) && tma_kv != 0)) ++gathered;
+  // this warp's 32 entries of tile t of list s, -1 past its end; the first
+  // quarter's warp also takes the others, for the tile's contiguity
+  struct Entries {
+    int s, j0, n, raw[4];
+  };
+  auto load = [&](int s, int t, Entries& x) {
+    x.s = s;
+    x.j0 = t * pf::BN;
+    x.n = kv_len ? min(max(__ldg(kv_len + s), 0), L) : L;
+    const int32_t* rows = kv_rows + (size_t)s * L + x.j0;
+    #pragma unroll
+    for (int q = 0; q < 4; ++q)
+      x.raw[q] = (q == 0 || quarter == 0) && x.j0 + (quarter + q) * 32 + lane < L ? __ldg(rows + (quarter + q) * 32 + lane) : -1;
+  };
+  auto entry = [&](const Entries& x, int q) {
+    const int r = x.raw[q];
+    return (x.j0 + (quarter + q) * 32 + lane < x.n && r >= 0 && (long long)r < R) ? r : -1;
+  };
+  Entries cur, nxt;
+  int s = 0, t = 0;
+  if (first < all) {
+    s = (int)(first / tiles_per);
+    t = (int)(first % tiles_per);
+    load(s, t, cur);
+  }
+  for (long long u = first; u < all; u += step) {
+    // the next tile's entries, under way while this one's rows are read
+    s += ds;
+    t += dt;
+    if (t >= tiles_per) {
+      t -= tiles_per;
+      ++s;
     }
-    uint4 w[16];
-    if constexpr (HEADS) {
-      // one row of 16 chunks per half warp, all 32 rows' loads issued before any is examined
-      const uint4* vh = v + (s % heads) * (pf::HD / 8) + (lane & 15);
-      #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const int row = __shfl_sync(0xffffffffu, own, 2 * u + (lane >> 4));
-        w[u] = row >= 0 ? __ldg(vh + (size_t)row * row_chunks) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      #pragma unroll
-      for (int u = 0; u < 16; ++u) examine(w[u]);
-    } else {
-      // eight rows at a time, each read by the whole warp, 1 KB of each
-      for (int rr = 0; rr < 32; rr += 8) {
-        for (int i0 = 0; i0 < row_chunks; i0 += 64) {
-          #pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const int row = __shfl_sync(0xffffffffu, own, rr + (u >> 1)), i = i0 + (u & 1) * 32 + lane;
-            w[u] = (row >= 0 && i < row_chunks) ? __ldg(v + (size_t)row * row_chunks + i) : make_uint4(0u, 0u, 0u, 0u);
+    if (u + step < all) load(s, t, nxt);
+    if (cur.j0 < cur.n) {
+      const int own = entry(cur, 0);
+      uint4 w[16];
+      if constexpr (HEADS) {
+        // one row of 16 chunks per half warp, all 32 rows' loads issued before any is examined
+        const uint4* vh = v + (cur.s % heads) * (pf::HD / 8) + (lane & 15);
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = __shfl_sync(0xffffffffu, own, 2 * i + (lane >> 4));
+          w[i] = row >= 0 ? __ldg(vh + (size_t)row * row_chunks) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) examine(w[i]);
+      } else {
+        // eight rows at a time, each read by the whole warp, 1 KB of each
+        for (int rr = 0; rr < 32; rr += 8) {
+          for (int i0 = 0; i0 < row_chunks; i0 += 64) {
+            #pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int row = __shfl_sync(0xffffffffu, own, rr + (k >> 1)), i = i0 + (k & 1) * 32 + lane;
+              w[k] = (row >= 0 && i < row_chunks) ? __ldg(v + (size_t)row * row_chunks + i) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            #pragma unroll
+            for (int k = 0; k < 16; ++k) examine(w[k]);
           }
-          #pragma unroll
-          for (int u = 0; u < 16; ++u) examine(w[u]);
         }
       }
+      if (quarter == 0) {
+        const int r[4] = {own, entry(cur, 1), entry(cur, 2), entry(cur, 3)};
+        int r0, r1;
+        ++tiles;
+        if (!(half_runs(r, lane, r0, r1) && tma_kv != 0)) ++gathered;
+      }
     }
+    cur = nxt;
   }
-  if (__any_sync(0xffffffffu, bad != 0) && lane == 0) atomicOr(words, 1u);
+  if (__any_sync(0xffffffffu, (bad & 0x80008000u) != 0) && lane == 0) atomicOr(sums, 1u);
   if (lane == 0 && tiles) {
-    atomicAdd(words + 1, gathered);
-    atomicAdd(words + 2, tiles);
+    atomicAdd(sums + 1, gathered);
+    atomicAdd(sums + 2, tiles);
+  }
+  __syncthreads();
+  if (threadIdx.x < 3 && sums[threadIdx.x]) {
+    if (threadIdx.x == 0) atomicOr(words, 1u);
+    else atomicAdd(words + threadIdx.x, sums[threadIdx.x]);
   }
 }
 
@@ -859,7 +905,7 @@ cudaError_t prefill_launch(const PrefillParams& a, cudaStream_t st) {
     const long long blocks = (tiles + 1) / 2;
     if (blocks > 0) {
       auto scan = a.head_lists ? prefill_v_scan_kernel<true> : prefill_v_scan_kernel<false>;
-      scan<<<(unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(
+      scan<<<(unsigned)(blocks < 152 * kScanPerSm ? blocks : 152 * kScanPerSm), 256, 0, st>>>(
           static_cast<const uint4*>(a.v), a.kv_rows, a.kv_len, (int)nl, a.L, a.R, a.Hkv * pf::HD / 8, a.head_lists ? a.Hkv : 1, kp.tma_kv,
           a.err + 1);
       e = cudaGetLastError();
