@@ -109,7 +109,7 @@ __host__ __device__ inline KsLayout ks_layout(int nv) {
   l.code = QUANT ? ks::BM * kv_row_bytes<KIND>(D) : 0;
   l.off_q = 0;
   l.off_k = (2 * l.qb_bytes + 1023) / 1024 * 1024;
-  const int room = ks::SMEM_MAX - 1024 - l.off_k - 3072;
+  const int room = ks::SMEM_MAX - 1024 - l.off_k - 3 * 1024;
   if (QUANT) {
     // the code ring, operand stages with what is left (two at least; one for D 256)
     l.ncs = ks::kGroups<D, 1, true> * (ks_ahead<D, KIND>() + 1);
@@ -182,6 +182,12 @@ __device__ __forceinline__ void ks_next(const KeyScanParams& p, Walk& w) {
 __device__ __forceinline__ float max_nan2(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -861,13 +867,15 @@ struct Shape {
   static constexpr int NMMA = SC && NST < 2 * NK ? 1 : 2;
   static constexpr int NEPI = 4 * NT, W_MMA = NEPI, W_Q = NEPI + NMMA, NQW = SC ? 8 : 1;
   static constexpr int THREADS = (W_Q + NQW) * 32;
+  static constexpr int NQG = SC ? NST / NK : 1;            // groups of query warps
   static constexpr int OFF_Q = NT * NK * KMAT;
   static constexpr int OFF_BAR = OFF_Q + NST * QST;
   static constexpr int NBAR = 2 + 2 * NST + 2 * NBUF + NMMA + 2 * NL;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_L = (OFF_MISC + 16 + 15) / 16 * 16;     // [NL][N] lse, [NL][N] limits, [NL] flags
   static constexpr int OFF_IDX = OFF_L + (SC ? 0 : NL * N * 8 + NL * 4);
-  static constexpr int USED = OFF_IDX + NT * ks::BM * 4;
+  static constexpr int OFF_ROW = OFF_IDX + NT * ks::BM * 4;        // [N] scores: query rows of a slice's first tile
+  static constexpr int USED = OFF_ROW + (SC ? N * 4 : 0);
   static constexpr int SMEM = USED + 1024;
   static constexpr uint32_t COLS = NBUF * N;
   static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0 && NBUF >= NT && NBUF == 4, "tensor memory");
@@ -907,6 +915,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
   int* lim = reinterpret_cast<int*>(nl2 + NL * N);
   int* odd = lim + NL * N;               // a column of the tile adds nothing, whatever its product
   int* idx = reinterpret_cast<int*>(sm + Sh::OFF_IDX);
+  int* qrow = reinterpret_cast<int*>(sm + Sh::OFF_ROW);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool bf16 = p.q_bf16 != 0;
@@ -938,7 +947,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     mbar_init(key_full, Sh::NEPI * 32);
     mbar_init(key_seen, NMMA);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(q_full + i, MODE == SCAN_SCORES ? Sh::NQW : 1);
+      mbar_init(q_full + i, Sh::NQW / Sh::NQG);
       mbar_init(q_empty + i, MODE == SCAN_SCORES ? 1 : NMMA);
     }
     for (int i = 0; i < NL; ++i) {
@@ -957,6 +966,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     tmem_alloc(tmem_holder, Sh::COLS);
     tmem_relinquish();
   }
+  if (MODE == SCAN_SCORES && tid < N) qrow[tid] = tid / p.G * p.Hq + tid % p.G;
   if (MODE == SCAN_WEIGHTS && pl.q_box * p.G < N) {
     // rows of a query tile that no box writes
     for (int f = tid; f < NST * Sh::QST / 16; f += Sh::THREADS)
@@ -1048,7 +1058,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       }
       float old = 0.f;
       if (MODE == SCAN_WEIGHTS && p.decay != 0.f && j < n) old = __ldcg(out + j);
-      float total = MODE == SCAN_SCORES ? -INF : 0.f;
+      float total = MODE == SCAN_SCORES ? -INF : 0.f, total2 = -INF;   // scores: their maximum is the result
       const int kn = T > 0 ? key_tiles(n) : 0;
       for (int t = 0; t < T; ++t) {
         const int sl = lround % NL;
@@ -1090,7 +1100,10 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
           if constexpr (MODE == SCAN_SCORES) {
             if (m >= N) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) total = max_nan2(total, __uint_as_float(y[i]));
+              for (int i = 0; i < 32; i += 4) {
+                total = max_nan3(total, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                total2 = max_nan3(total2, __uint_as_float(y[i + 2]), __uint_as_float(y[i + 3]));
+              }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
@@ -1137,7 +1150,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
       if (j < n) {
         if (MODE == SCAN_SCORES) {
-          out[j] = row >= 0 ? total : -INF;
+          out[j] = row >= 0 ? max_nan2(total, total2) : -INF;
         } else {
           const float add = row >= 0 ? total : 0.f;
           out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);
@@ -1263,63 +1276,70 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     }
   } else {
     // ------------------------------------------------------------ queries, split by sign
-    constexpr int CPR = D / 8, STEP = Sh::NQW * 32, NX = N * CPR / STEP;
-    const int qt = tid - Sh::W_Q * 32;
+    // Two groups of four warps on alternate query tiles, each with a pair of
+    // stages of its own (and an issuing warp that it alone feeds): the waits and
+    // fences of one lie under the other's stores (16 x 128 queries, 1,562 blocks:
+    // 54 us, 58 with all eight warps at every tile).  At D 256 one group of
+    // eight, as there is one pair.  Measured besides: the bounds in tensor
+    // memory instead of shared memory, 55 us (a query tile 0.70 us for 0.76, but
+    // a CTA starts 1 us later); all eight warps with two tiles of loads in
+    // flight, 61 us.
+    constexpr int CPR = D / 8, GW = Sh::NQW / Sh::NQG, STEP = GW * 32, NX = N * CPR / STEP;
+    const int grp = (warp - Sh::W_Q) / GW, qt = (tid - Sh::W_Q * 32) % STEP;
     const uint16_t* qg = static_cast<const uint16_t*>(p.q);
-    // this thread's 16-byte words of a query tile, and the query rows
-    // (query * Hq + head) that they are of; where whole queries fill a tile,
-    // the next tile's rows are a fixed number further on
+    // This thread's 16-byte words of a query tile.  qrow holds the query rows
+    // (query * Hq + head) of a slice's first tile; where whole queries fill a
+    // tile, the rows of tile t are t * pitch further on.
     uint4 x[NX];
-    int at[NX];
-    const bool whole = N % p.G == 0;
     const int pitch = N / p.G * p.Hq;
-    auto locate = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < NX; ++i) {
-        const int v = min(t * N + (i * STEP + qt) / CPR, p.NV - 1);
-        at[i] = v / p.G * p.Hq + v % p.G;
-      }
-    };
     auto fetch = [&](int s, int t) {
-      if (t == 0 || !whole || (t + 1) * N > p.NV) {
-        locate(t);
-      } else {
+      const uint16_t* base = qg + ((size_t)s * p.Nq * p.Hq + g * p.G) * D + (qt % CPR) * 8;   // STEP is a multiple of CPR
+      if (N % p.G == 0 && (t + 1) * N <= p.NV) {
+        base += (size_t)t * pitch * D;
 #pragma unroll
-        for (int i = 0; i < NX; ++i) at[i] += pitch;
-      }
-      const uint16_t* base = qg + ((size_t)s * p.Nq * p.Hq + g * p.G) * D;
+        for (int i = 0; i < NX; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)qrow[(i * STEP + qt) / CPR] * D));
+      } else {   // past the last query: zeros
 #pragma unroll
-      for (int i = 0; i < NX; ++i)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)at[i] * D) + (i * STEP + qt) % CPR);
-      if ((t + 1) * N > p.NV) {   // past the last query: zeros
-#pragma unroll
-        for (int i = 0; i < NX; ++i)
-          if (t * N + (i * STEP + qt) / CPR >= p.NV) x[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    bool ok = true;
-    Ring qr;
-    for (int s = s_lo; ok && s < s_hi; ++s) {
-      if (first_tile(ks_entries<MODE>(p, s)) == nt) continue;
-      fetch(s, 0);
-      for (int t = 0; ok && t < nt; ++t) {
-#pragma unroll
-        for (int m = 0; m < NK; ++m) {
-          const int st = qr.st;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, qr.ph ^ 1u, abort_flag, wait_ns)))) break;
-          qr.next(NST);
-          unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
-#pragma unroll
-          for (int i = 0; i < NX; ++i) {
-            const int f = i * STEP + qt, r = f / CPR, c = f % CPR;
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x[i], m == 0, bf16);
-          }
-          if (m == NK - 1 && t + 1 < nt) fetch(s, t + 1);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full + st);
+        for (int i = 0; i < NX; ++i) {
+          const int v = t * N + (i * STEP + qt) / CPR;
+          x[i] = v < p.NV ? __ldg(reinterpret_cast<const uint4*>(base + (size_t)(v / p.G * p.Hq + v % p.G) * D))
+                           : make_uint4(0u, 0u, 0u, 0u);
         }
       }
+    };
+    // over the query tiles of all slices that have such blocks
+    int s = s_lo, t = 0;
+    auto enter = [&]() {
+      while (s < s_hi && first_tile(ks_entries<MODE>(p, s)) == nt) ++s;
+    };
+    auto next = [&]() {
+      if (++t < nt) return;
+      t = 0;
+      ++s;
+      enter();
+    };
+    enter();
+    for (int i = 0; i < grp; ++i) next();
+    if (s < s_hi) fetch(s, t);
+    bool ok = true;
+    for (int k = 0; ok && s < s_hi; ++k) {
+#pragma unroll
+      for (int i = 0; i < Sh::NQG; ++i) next();
+#pragma unroll
+      for (int m = 0; m < NK; ++m) {
+        const int st = grp * NK + m;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(q_empty + st, (k & 1) ^ 1, abort_flag, wait_ns)))) break;
+        unsigned char* dst = sm + Sh::OFF_Q + st * Sh::QST;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          const int f = i * STEP + qt, r = f / CPR, c = f % CPR;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = sign_part(x[i], m == 0, bf16);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + st);
+      }
+      if (s < s_hi) fetch(s, t);
     }
   }
 
