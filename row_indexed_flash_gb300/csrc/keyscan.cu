@@ -75,6 +75,12 @@ constexpr int SMEM_MAX = 225 * 1024;
 // (scores), codes or D 256 only 64 vectors leave room for the stages.
 template <int D, int NK, bool QUANT>
 constexpr int kStreamVec = NK == 1 && !QUANT && D <= 128 ? 128 : 64;
+// Accumulators per tile: at D 256 the two products of a score have one each and
+// are added in fp32.  The tensor core cuts its running sum off rather than
+// rounding it, and the terms of a score mostly have one sign, so 32 steps into
+// one accumulator left f16 scores 1.6e-6 low; 16 into each of two leave half that.
+template <int D, int NK>
+constexpr int kParts = NK == 2 && D == 256 ? 2 : 1;
 }  // namespace ks
 
 namespace {
@@ -272,6 +278,7 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
   constexpr bool QUANT = KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8;
   constexpr int NK = MODE == SCAN_SCORES ? 2 : 1;   // stages per tile
   constexpr int NKEY = kKeyWarps<QUANT>;
+  constexpr int PARTS = kParts<D, NK>;
   constexpr int ATOM = BM * 128;                    // one 64-column atom of a key tile
   constexpr int KT = D / 64;
   const float INF = __int_as_float(0x7f800000);
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
     mbar_fence_init();
   }
   uint32_t ncols = 32;
-  while ((int)ncols < NBUF * N) ncols <<= 1;
+  while ((int)ncols < NBUF * PARTS * N) ncols <<= 1;
   if (warp == W_MMA) {
     tmem_alloc(tmem_holder, ncols);
     tmem_relinquish();
@@ -471,7 +478,13 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
       for (int u = 0; u < 4; ++u) r[u] = MODE == SCAN_SCORES ? -INF : 0.f;
       for (int c0 = 0; c0 < N; c0 += 16) {
         uint32_t x[16];
-        tmem_ld16(tbase + lanes + b * N + c0, x);
+        tmem_ld16(tbase + lanes + b * PARTS * N + c0, x);
+        if constexpr (PARTS == 2) {
+          uint32_t y[16];
+          tmem_ld16(tbase + lanes + (b * PARTS + 1) * N + c0, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+        }
         if (MODE == SCAN_SCORES) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -560,8 +573,8 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
           fence_proxy_async_smem();   // the stage's cp.async copies arrived by themselves
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
-            mma_ss(tbase + sr.st * N, sdesc_at(a, (i >> 2) * ATOM + (i & 3) * 32), sdesc_at(q, (i >> 2) * qatom + (i & 3) * 32),
-                   id, m > 0 || i > 0);
+            mma_ss(tbase + (sr.st * PARTS + m % PARTS) * N, sdesc_at(a, (i >> 2) * ATOM + (i & 3) * 32),
+                   sdesc_at(q, (i >> 2) * qatom + (i & 3) * 32), id, m >= PARTS || i > 0);
           tc_commit(k_empty + st);
           if (m == NK - 1) {
             tc_commit(s_full + sr.st);
@@ -877,7 +890,8 @@ struct Shape {
   static constexpr int OFF_ROW = OFF_IDX + NT * ks::BM * 4;        // [N] scores: query rows of a slice's first tile
   static constexpr int USED = OFF_ROW + (SC ? N * 4 : 0);
   static constexpr int SMEM = USED + 1024;
-  static constexpr uint32_t COLS = NBUF * N;
+  static constexpr int PARTS = ks::kParts<D, NK>;
+  static constexpr uint32_t COLS = NBUF * PARTS * N;
   static_assert(COLS <= 512 && (COLS & (COLS - 1)) == 0 && NBUF >= NT && NBUF == 4, "tensor memory");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -1075,7 +1089,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         }
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(s_full + b, phase, abort_flag, wait_ns)))) break;
         tc_fence_after();
-        const uint32_t at = tbase + lanes + b * N;
+        const uint32_t at = tbase + lanes + b * Sh::PARTS * N;
         const int m = p.NV - t * N;      // scores: real columns of the tile
         const float4* l4 = reinterpret_cast<const float4*>(nl2 + sl * N);
         const int4* m4 = reinterpret_cast<const int4*>(lim + sl * N);
@@ -1085,13 +1099,22 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         const float2 cs2 = make_float2(cs, cs);
         // 32 columns at a time, the next ones' load under way meanwhile
         uint32_t x[2][32];
-        tmem_ld32(at, x[0]);
+        if constexpr (Sh::PARTS == 1) tmem_ld32(at, x[0]);
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) {
-          uint32_t(&y)[32] = x[c & 1];
-          if (c > 0) tmem_wait_ld_tied(y);
+          uint32_t(&y)[32] = x[Sh::PARTS == 2 ? 0 : c & 1];
+          if constexpr (Sh::PARTS == 2) {
+            tmem_ld32_nowait(at + 32 * c, y);
+            tmem_ld32_nowait(at + N + 32 * c, x[1]);
+            tmem_wait_ld_tied(y);
+            tmem_wait_ld_tied(x[1]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(x[1][i]));
+          } else if (c > 0) {
+            tmem_wait_ld_tied(y);
+          }
           if (c + 1 < N / 32) {
-            tmem_ld32_nowait(at + 32 * (c + 1), x[(c + 1) & 1]);
+            if constexpr (Sh::PARTS == 1) tmem_ld32_nowait(at + 32 * (c + 1), x[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
@@ -1176,8 +1199,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tbase + b * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
-                 sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m > 0 || i > 0);
+          mma_ss(tbase + (b * Sh::PARTS + m % Sh::PARTS) * N, sdesc_at(a, (i >> 2) * Sh::ATOM + (i & 3) * 32),
+                 sdesc_at(q, (i >> 2) * (N * 128) + (i & 3) * 32), id, m >= Sh::PARTS || i > 0);
         if (m == NK - 1) tc_commit(s_full + b);
       }
       __syncwarp();

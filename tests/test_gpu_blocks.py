@@ -343,3 +343,22 @@ def test_scores_of_many_slices_of_alternating_sequences():
         lens = g.integers(0, 64 * 130, size=S)
         lens[::9] = 0
         check_scores(*score_case(151 + Nq, S=S, Nq=Nq, Hq=8, Hkv=2, D=128, P=140, NB=130, lens=lens, slice_seq=seq, n_seq=3))
+
+
+@pytest.mark.parametrize("D, Nq", [(64, 1), (128, 1), (256, 1), (128, 70), (256, 70)])
+def test_scores_are_not_biased_low(D, Nq):
+    """Terms of one sign: a running sum that is cut off, not rounded, ends low.
+
+    A step of 16 products cuts off less than 2^-23 of the sum so far; over n equal steps that is
+    (n + 1) / 2 * 2^-23 of the result.  One accumulator takes both products up to D 128 (D / 8 steps),
+    two take 16 steps each at D 256; one fp32 addition more rounds by 2^-24.
+    """
+    g = synth.rng(90 + D + Nq)
+    q = synth.normal_bits(g, (1, Nq, 8, D), "f16")
+    size = [np.abs(widen(synth.normal_bits(g, (150, 2, D), "f16"), "f16")) + 1 for _ in range(2)]
+    lo, hi = (synth.f32_to_f16_bits(np.asarray(x, np.float32)) for x in (-size[0], size[1]))
+    table, lens = np.arange(150, dtype=np.int32)[None], np.asarray([150 * 64], np.int32)
+    got = check_scores(q, lo, hi, table, lens, None, "f16")
+    want = oracle.block_scores(widen(q, "f16"), widen(lo, "f16"), widen(hi, "f16"), table, lens, None)
+    steps = min(D // 8, 16)
+    assert abs(((got - want) / want).mean()) < ((steps + 1) / 2 * 2.0 + 1) * 2.0 ** -24
