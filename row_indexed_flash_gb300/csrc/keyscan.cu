@@ -1000,8 +1000,11 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const int e = tid & 127;
     const int j = kt < tile_end - tile0 ? j0 + kt * BM + e : p.L;   // past every entry where the batch has no such tile
-    int* my_idx = idx + kt * BM;
-    unsigned char* kdst = sm + kt * NK * Sh::KMAT;
+    // Each warp stages its own 32 keys, so that no barrier between warps stands
+    // behind a wait that some of them may have given up.
+    const int key0 = (warp & 3) * 32;
+    int* my_idx = idx + kt * BM + key0;
+    unsigned char* kdst = sm + kt * NK * Sh::KMAT + key0 * 128;   // 32 rows are four whole swizzle periods
     int loaded = -1, loads = 0, row = -1;
     float cs = p.c;
     int round = 0, lround = 0;                             // query tiles and lse slots so far
@@ -1025,23 +1028,23 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         loaded = list;
         row = j < (MODE == SCAN_SCORES ? p.L : n) ? __ldg(p.rows + (size_t)list * p.L + j) : -1;
         row = row >= 0 && (long long)row < p.R ? row : -1;
-        my_idx[e] = row;
-        named_barrier(1 + kt, 128);
+        my_idx[lane] = row;
+        __syncwarp();
         if constexpr (QUANT) {
           constexpr int CB = kv_row_bytes<KIND>(D), CPR = CB / 16, W = KvChunk<KIND>::N / 8;
           constexpr int B = CPR < 8 ? CPR : 8;   // chunks per thread and step, all loaded before any is widened
           const char* src = static_cast<const char*>(p.k[0]) + (size_t)g * CB;
           const size_t pitch = (size_t)p.Hkv * CB;
-          for (int f0 = e; f0 < BM * CPR; f0 += B * BM) {
+          for (int f0 = lane; f0 < 32 * CPR; f0 += B * 32) {
             uint4 y[B];
 #pragma unroll
             for (int u = 0; u < B; ++u) {
-              const int f = f0 + u * BM, r = my_idx[f / CPR];
+              const int f = f0 + u * 32, r = my_idx[f / CPR];
               y[u] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + r * pitch) + f % CPR) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int u = 0; u < B; ++u) {
-              const int f = f0 + u * BM, k = f / CPR, c = f % CPR;
+              const int f = f0 + u * 32, k = f / CPR, c = f % CPR;
               uint4 o[W];
               widen_chunk<KIND>(y[u], bf16, o);
 #pragma unroll
@@ -1061,7 +1064,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
             const char* src = static_cast<const char*>(p.k[m]) + (size_t)g * (D * 2);
             const size_t pitch = (size_t)p.Hkv * (D * 2);
 #pragma unroll 8
-            for (int f = e; f < BM * CPR; f += BM) {
+            for (int f = lane; f < 32 * CPR; f += 32) {
               const int k = f / CPR, c = f % CPR, r = my_idx[k];
               cp_async16(kdst + m * Sh::KMAT + (c >> 3) * Sh::ATOM + k * 128 + (((c & 7) ^ (k & 7)) << 4),
                          src + max(r, 0) * pitch + c * 16, r >= 0);

@@ -362,3 +362,23 @@ def test_scores_are_not_biased_low(D, Nq):
     want = oracle.block_scores(widen(q, "f16"), widen(lo, "f16"), widen(hi, "f16"), table, lens, None)
     steps = min(D // 8, 16)
     assert abs(((got - want) / want).mean()) < ((steps + 1) / 2 * 2.0 + 1) * 2.0 ** -24
+
+
+def test_scores_report_an_expired_wait_and_recover():
+    """Every wait of the prompt form runs out in turn, in CTAs that stage the bounds of several sequences."""
+    g = synth.rng(170)
+    S = 60
+    q, lo, hi, table, lens, seq, _ = score_case(171, S=S, Nq=17, Hq=32, Hkv=8, D=128, P=140, NB=130,
+                                                lens=g.integers(64, 64 * 130, size=S), slice_seq=np.arange(S) % 3, n_seq=3)
+    q, lo, hi = (dev_bits(x, "bf16") for x in (q, lo, hi))
+    table, lens, seq = cuda(table), cuda(lens), cuda(seq)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = far.fa_kv_block_scores(q, lo, hi, table, lens, slice_seq=seq, workspace=ws, check_status=True)
+    try:
+        for limit in (1, 1000, 4000, 16000):
+            far.fa_set_wait_limit_ns(limit)
+            far.fa_kv_block_scores(q, lo, hi, table, lens, slice_seq=seq, workspace=ws)
+            assert far.fa_rows_status(ws, clear=True) & far.FA_WS_WAIT_EXPIRED or limit > 1
+    finally:
+        far.fa_set_wait_limit_ns(0)
+    assert torch.equal(far.fa_kv_block_scores(q, lo, hi, table, lens, slice_seq=seq, workspace=ws, check_status=True), want)
