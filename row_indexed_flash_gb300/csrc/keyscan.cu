@@ -403,6 +403,10 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  // Key warps of 16-bit pools: stages filled so far, and (the lane that issues
+  // them) the stages whose last fill was TMA loads, with its phase parity.
+  int fills = 0;
+  unsigned tma_pend = 0, tma_par = 0;
 
   if (warp < NEPI) {
     // ------------------------------------------------------------ reduction
@@ -681,7 +685,6 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
     auto row_of = [&](int r) { return r >= 0 && (long long)r < p.R ? r : -1; };
     if constexpr (!QUANT) {
       constexpr int CPR = D / 8;
-      unsigned tma_pend = 0, tma_par = 0;
       const int half = kw / (GW / 2), sub = kw % (GW / 2);   // 64-row half of the tile, RW rows of it
       // List entries PRE tiles ahead (a tile's share of HBM time is shorter
       // than the latency of a list load), in register sets that the unrolled
@@ -712,6 +715,8 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
             const int st = kr.st;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(k_empty + st, kr.ph ^ 1u, abort_flag, wait_ns)))) break;
             unsigned char* dst = sm + ly.off_k + st * ly.tile + half * 64 * 128;
+            tma_pend &= ~(1u << st);
+            ++fills;
             if (run) {
               if (sub == 0 && lane == 0) {
                 mbar_arrive_expect_tx(k_full + st, 64 * D * 2);
@@ -744,10 +749,6 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
         }
       }
       cp_async_wait_all();
-      if (*abort_flag && sub == 0 && lane == 0) {   // no TMA load may still be writing when the CTA exits
-        for (int i = 0; i < NST; ++i)
-          if ((tma_pend >> i) & 1u) ks_wait_drain(k_full + i, (tma_par >> i) & 1u);
-      }
     } else {
       // RW rows of each of the group's tiles per warp; each lane copies, and
       // later widens, its own 16-byte chunks, which lie lane by lane in the code ring
@@ -837,7 +838,26 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
     tc_fence_after();
     tmem_dealloc(tbase, ncols);
   }
-  if (tid == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+  if (*abort_flag) {   // final: every role has ended
+    if (tid == 0 && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+    if constexpr (!QUANT) {
+      // No TMA load may still be writing when the CTA exits.  A stage's barrier
+      // tells of its loads only once every warp of the group has arrived, so the
+      // warps that gave up first arrive for the fills that others made after it.
+      int* most = reinterpret_cast<int*>(l2);   // fills of each group's furthest warp
+      constexpr int GROUPS = kGroups<D, NK, QUANT>, GW = NKEY / GROUPS;
+      const int grp = (warp - W_KEY) / GW;
+      if (tid < GROUPS) most[tid] = 0;
+      __syncthreads();
+      if (warp >= W_KEY && lane == 0) atomicMax(most + grp, fills);
+      __syncthreads();
+      if (warp >= W_KEY) {
+        for (int u = fills; u < most[grp]; ++u) mbar_arrive(k_full + ((u / NK * GROUPS + grp) * NK + u % NK) % NST);
+        for (int i = 0; i < NST; ++i)
+          if ((tma_pend >> i) & 1u) ks_wait_drain(k_full + i, (tma_par >> i) & 1u);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -991,6 +1011,7 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
+  unsigned pend = 0, par = 0;   // weights, the lane that loads queries: stages with a TMA load, and its phase parity
   // the list (page table row) of a slice
   auto list_of_slice = [&](int s) { return MODE == SCAN_SCORES && p.slice_seq ? __ldg(p.slice_seq + s) : s; };
 
@@ -1250,7 +1271,6 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     // ------------------------------------------------------------ queries by TMA
     const int s = s_lo, n = ks_entries<MODE>(p, s), PT = pl.PT;
     const int t0 = first_tile(n), T = nt - t0;
-    unsigned pend = 0, par = 0;
     // This lane's columns v = lane + 32 u of a query tile: query v / G, head v % G.
     // The next tile's lse are loaded as they stand and looked at when it is that tile's turn.
     const float* lse_at[N / 32];
@@ -1295,10 +1315,6 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
       if (lane == 0) odd[sl] = hide;
       __syncwarp();
       if (lane == 0) mbar_arrive(l_full + sl);
-    }
-    if (*abort_flag && lane == 0) {   // no TMA load may still be writing when the CTA exits
-      for (int i = 0; i < NST; ++i)
-        if ((pend >> i) & 1u) ks_wait_drain(q_full + i, (par >> i) & 1u);
     }
   } else {
     // ------------------------------------------------------------ queries, split by sign
@@ -1376,7 +1392,13 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     tc_fence_after();
     tmem_dealloc(tbase, Sh::COLS);
   }
-  if (tid == 0 && *abort_flag && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+  if (*abort_flag) {   // final: every role has ended
+    if (tid == 0 && p.err) atomicOr(p.err, FA_WS_WAIT_EXPIRED);
+    // No TMA load may still be writing when the CTA exits.  The lane that issued
+    // a stage's loads makes its only arrival, so the loads alone are waited for.
+    for (int i = 0; i < NST; ++i)
+      if ((pend >> i) & 1u) ks_wait_drain(q_full + i, (par >> i) & 1u);
+  }
 }
 
 // ---------------------------------------------------------------------------

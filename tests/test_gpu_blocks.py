@@ -1,4 +1,6 @@
 """Block bounds, block scores, block row lists and attention over one list per KV head, against the fp64 oracle."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -382,3 +384,28 @@ def test_scores_report_an_expired_wait_and_recover():
     finally:
         far.fa_set_wait_limit_ns(0)
     assert torch.equal(far.fa_kv_block_scores(q, lo, hi, table, lens, slice_seq=seq, workspace=ws, check_status=True), want)
+
+
+@pytest.mark.parametrize("D,together", [(128, True), (128, False), (256, True), (64, True)])
+def test_scores_of_one_token_drain_after_an_expired_wait(D, together):
+    """The streaming form, with tile copies (tables of consecutive pages) and with gathers."""
+    q, lo, hi, table, lens, _, _ = score_case(180 + D, S=5, Nq=1, Hq=8, Hkv=2, D=D, P=6000, NB=1100, lens=[1100 * 64] * 5)
+    if together:
+        table[:] = np.arange(1100) + 1000 * np.arange(5)[:, None] - 300 * (np.arange(5)[:, None] > 3)
+        table[:, 300:700:130] = 7                        # pages that break some of the runs
+    q, lo, hi = (dev_bits(x, "bf16") for x in (q, lo, hi))
+    table, lens = cuda(table), cuda(lens)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = far.fa_kv_block_scores(q, lo, hi, table, lens, workspace=ws, check_status=True)
+    spent = []
+    try:
+        for limit in (1, 1, 300, 1000, 3000):
+            far.fa_set_wait_limit_ns(limit)
+            begun = time.monotonic()
+            far.fa_kv_block_scores(q, lo, hi, table, lens, workspace=ws)
+            assert far.fa_rows_status(ws, clear=True) & far.FA_WS_WAIT_EXPIRED or limit > 1
+            spent.append(time.monotonic() - begun)
+    finally:
+        far.fa_set_wait_limit_ns(0)
+    assert torch.equal(far.fa_kv_block_scores(q, lo, hi, table, lens, workspace=ws, check_status=True), want)
+    assert max(spent) < 0.5, spent

@@ -6,6 +6,8 @@ most e = (D + 8) * 2^-23 * scale * sum_d |q_d k_d| + 2^-22 * (|x| + |lse| + 1)
 2^-23 a step, since the tensor core's sums need not round to nearest), the
 hardware exponential 2^-21, and the sum of nv terms nv * 2^-24 of itself.
 """
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -291,3 +293,32 @@ def test_weights_of_long_prompts(kv, Nq, L, G):
                                   k_scale=ks, check_status=True)[0].double()
         # each term: exponent error below 2^-23 * ((D + 8) * 8 + 60) ~ 1.4e-4 for |scale q k| sums below 8, |x| + |lse| below 30
         assert ((got - want).abs() <= 1.4e-4 * want + 1e-35).all(), ((got - want).abs() / want.clamp(min=1e-30)).max()
+
+
+@pytest.mark.parametrize("Nq,G,L", [(1, 4, 6000), (1, 4, 700), (40, 4, 6000), (40, 4, 130), (70, 1, 3000)])
+def test_an_expired_wait_leaves_no_copy_behind(Nq, G, L):
+    """Lists of whole pages (tile copies) with shuffled ones between (gathers), few tiles and many.
+
+    A call whose waits run out drains its own copies before it ends: that takes microseconds, not the second
+    after which a drain gives up, as it would if it waited for a warp that had left.
+    """
+    p, kd, _, _ = make(360 + L + Nq, "bf16", S=2, Nq=Nq, Hq=2 * G, Hkv=2, D=128, R=16384, L=L)
+    rows = paged_rows(361, 2, -(-L // 64) * 64, 16384, 64).reshape(2, -1, 64)
+    rows[:, 2::3] = rows[:, 2::3, ::-1]
+    rows = torch.from_numpy(np.ascontiguousarray(rows.reshape(2, -1)[:, :L])).cuda()
+    lse = torch.zeros((2, Nq, 2 * G), dtype=torch.float32, device="cuda")
+    q = dev_bits(p.q, "bf16")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    want = far.fa_rows_weights(q, kd, rows, p.scale, lse, workspace=ws, check_status=True)
+    spent = []
+    try:
+        for limit in (1, 1, 300, 1000, 3000):
+            far.fa_set_wait_limit_ns(limit)
+            begun = time.monotonic()
+            far.fa_rows_weights(q, kd, rows, p.scale, lse, workspace=ws)
+            assert far.fa_rows_status(ws, clear=True) & far.FA_WS_WAIT_EXPIRED or limit > 1
+            spent.append(time.monotonic() - begun)
+    finally:
+        far.fa_set_wait_limit_ns(0)
+    assert torch.equal(far.fa_rows_weights(q, kd, rows, p.scale, lse, workspace=ws, check_status=True), want)
+    assert max(spent) < 0.5, spent
