@@ -390,8 +390,12 @@ fa_status fa_kv_block_bounds(const void* k, fa_dtype kv_dtype, const uint16_t* k
  *   score[s, g, b] = max over the slice's queries i and the heads h of group g of
  *                    sum_d max(q_d, 0) * kmax[page, g, d] + min(q_d, 0) * kmin[page, g, d],
  * which no dot product of one of those queries with a key of the block exceeds
- * (but for fp32 rounding).  Minus infinity for b >= ceil(seq_len[s] / 64) and
- * for page ids below 0 or at or past n_pool_pages; NaN where a term is NaN.
+ * (but for fp32 rounding).  A component takes the bound of its sign and a zero
+ * takes none, so an infinite bound (fa_kv_block_bounds rounds a key beyond the
+ * bounds' dtype to one) makes the score plus infinity or leaves it a number.
+ * Minus infinity for b >= ceil(seq_len[s] / 64) and for page ids below 0 or at
+ * or past n_pool_pages; NaN where q or a bound of the block is NaN, or where
+ * infinite terms of both signs meet.
  *   q          [S, Nq, Hq, D] and the bounds in the same dtype, D in {64,128,256}
  *   page_table [n_seq, max_pages] int32; slice s reads row slice_seq[s], or row s
  *              when slice_seq is NULL (several slices of one sequence: prompt tiles).

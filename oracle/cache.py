@@ -115,7 +115,12 @@ def block_bounds(k, pages, fill, kmin, kmax, fmt):
 
 
 def block_scores(q, kmin, kmax, page_table, seq_len, slice_seq: Optional[np.ndarray] = None):
-    """q, kmin, kmax float64; returns score [S, Hkv, max_pages]."""
+    """q, kmin, kmax float64; returns score [S, Hkv, max_pages].
+
+    A component takes the bound of its sign, a zero none, whatever the other
+    bound is; NaN where q or either bound is NaN, or infinite terms of both
+    signs meet.
+    """
     S, Nq, Hq, D = q.shape
     P, Hkv, _ = kmin.shape
     G = Hq // Hkv
@@ -133,7 +138,11 @@ def block_scores(q, kmin, kmax, page_table, seq_len, slice_seq: Optional[np.ndar
                 lo, hi = kmin[page, h // G], kmax[page, h // G]
                 for i in range(Nq):
                     x = q[s, i, h]
-                    best = float(np.where(x > 0, x * hi, x * lo).sum())
+                    with np.errstate(invalid="ignore"):
+                        term = np.where(x > 0, x * hi, np.where(x < 0, x * lo, x))
+                        best = float(term.sum())
+                    if np.isnan(lo).any() or np.isnan(hi).any():
+                        best = float("nan")
                     out[s, h // G, b] = best if best != best else max(out[s, h // G, b], best)
     return out
 

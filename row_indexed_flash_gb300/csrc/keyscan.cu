@@ -2,6 +2,7 @@
 //
 //   weights  acc[s, g, j] = decay * acc + sum_v exp2(c * <q_v, K[row_j, g]> - lse2_v)
 //   scores   score[s, g, b] = max_v <max(q_v, 0), kmax[page_b, g]> + <min(q_v, 0), kmin[page_b, g]>
+//            (an infinite bound counts only for the signs that use it: score_by_definition)
 //
 // Bound by the bytes of the keys: each is read once.  The keys of a tile are
 // the 128 rows of the MMA's M dimension and the few query vectors of the KV
@@ -270,6 +271,76 @@ __device__ __forceinline__ uint4 sign_part(const uint4& x, bool plus, bool bf16)
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+__device__ __forceinline__ float widen16(uint16_t x, bool bf16) {
+  return bf16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+
+// One score from its definition, by a warp.  The two products of the tensor core
+// put a zero against the bound that a component's sign does not use, and zero
+// times infinity is NaN: so a block with an infinite bound (a key of a quantised
+// pool beyond f16's range has one) comes out NaN where the score is a number.
+// A warp that sees a NaN forms that score again: here a component takes the
+// bound of its sign alone, and a zero takes none.  NaN where q or a bound is, or
+// where infinite terms of both signs meet.  q: the slice's first vector of the
+// KV head; hi, lo: the page's bounds.  Not inlined: hardly ever called.
+template <int D>
+__device__ __noinline__ float score_by_definition(const uint16_t* q, const uint16_t* hi, const uint16_t* lo, int NV, int G,
+                                                  int Hq, bool bf16) {
+  constexpr int PER = D / 32;
+  const int d0 = (threadIdx.x & 31) * PER;
+  const float NaN = __int_as_float(0x7fc00000);
+  float h[PER], l[PER];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    h[i] = widen16(__ldg(hi + d0 + i), bf16);
+    l[i] = widen16(__ldg(lo + d0 + i), bf16);
+    bad = bad || h[i] != h[i] || l[i] != l[i];
+  }
+  if (__any_sync(0xffffffffu, bad)) return NaN;
+  float best = __int_as_float(0xff800000);
+  constexpr int B = 4;   // vectors a step, for their latencies to overlap
+  for (int v0 = 0; v0 < NV; v0 += B) {
+    double sum[B];       // finite bf16 products reach beyond fp32
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int v = min(v0 + b, NV - 1);
+      const uint16_t* qv = q + (size_t)(v / G * Hq + v % G) * D + d0;
+      sum[b] = 0.;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float x = widen16(__ldg(qv + i), bf16);
+        sum[b] += x > 0.f ? (double)x * h[i] : x < 0.f ? (double)x * l[i] : (double)x;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], o);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      bad = bad || sum[b] != sum[b];
+      best = fmaxf(best, (float)sum[b]);
+    }
+    if (bad) return NaN;
+  }
+  return best;
+}
+// The scores of a warp's keys (lane = key, page its pool page, there: it has one), NaNs looked at again.
+template <int D>
+__device__ __forceinline__ float settle_scores(const KeyScanParams& p, int s, int g, float score, int page, bool there) {
+  for (unsigned nan = __ballot_sync(0xffffffffu, there && score != score); nan; nan &= nan - 1) {
+    const int src = __ffs(nan) - 1;
+    const size_t at = ((size_t)__shfl_sync(0xffffffffu, page, src) * p.Hkv + g) * D;
+    const float x = score_by_definition<D>(static_cast<const uint16_t*>(p.q) + ((size_t)s * p.Nq * p.Hq + g * p.G) * D,
+                                           static_cast<const uint16_t*>(p.k[0]) + at, static_cast<const uint16_t*>(p.k[1]) + at,
+                                           p.NV, p.G, p.Hq, p.q_bf16 != 0);
+    if ((int)(threadIdx.x & 31) == src) score = x;
+  }
+  return score;
+}
+
 template <int D, int MODE, int KIND>
 __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 || KIND == KV_F8>, 1)
     keyscan_stream_kernel(const KeyScanParams p, int tma_ok, const __grid_constant__ CUtensorMap t0,
@@ -528,8 +599,10 @@ __global__ void __launch_bounds__(ks::kThreads<KIND == KV_I8 || KIND == KV_I4 ||
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_empty + b);
-      if (MODE == SCAN_SCORES) {
-        if (j < w.n) out[j] = live(cur) ? max_nan2(max_nan2(r[0], r[1]), max_nan2(r[2], r[3])) : -INF;
+      if constexpr (MODE == SCAN_SCORES) {
+        const float best = settle_scores<D>(p, w.s, w.g, max_nan2(max_nan2(r[0], r[1]), max_nan2(r[2], r[3])), cur.row,
+                                            j < w.n && live(cur));
+        if (j < w.n) out[j] = live(cur) ? best : -INF;
         // past the sequence's blocks: the (slice, KV head)'s last tile fills the rest
         if (w.t + 1 == w.T)
           for (int f = w.n + kid; f < p.L; f += 128) out[f] = -INF;
@@ -1195,9 +1268,10 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
         }
       }
       if (!QUANT) cp_async_wait_all();   // also where no query tile sees these keys
+      if constexpr (MODE == SCAN_SCORES) total = settle_scores<D>(p, s, g, max_nan2(total, total2), row, ok && j < n && row >= 0);
       if (j < n) {
         if (MODE == SCAN_SCORES) {
-          out[j] = row >= 0 ? max_nan2(total, total2) : -INF;
+          out[j] = row >= 0 ? total : -INF;
         } else {
           const float add = row >= 0 ? total : 0.f;
           out[j] = p.decay == 0.f ? add : fmaf(p.decay, old, add);

@@ -409,3 +409,79 @@ def test_scores_of_one_token_drain_after_an_expired_wait(D, together):
         far.fa_set_wait_limit_ns(0)
     assert torch.equal(far.fa_kv_block_scores(q, lo, hi, table, lens, workspace=ws, check_status=True), want)
     assert max(spent) < 0.5, spent
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [1, 17, 70])
+def test_scores_of_infinite_bounds(D, Nq, dtype):
+    """One end or both infinite in some pages, under queries of either sign and zero there."""
+    q, lo, hi, table, lens, _, _ = score_case(190 + D + Nq, 2, Nq, 8, 2, D, 200, 140, [140 * 64, 139 * 64 - 5], dtype=dtype)
+    inf = 0x7F80 if dtype == "bf16" else 0x7C00
+    q[:, :, :, 3] |= 0x8000              # negative
+    q[:, :, :, 5] &= 0x7FFF              # positive
+    q[:, :, :, 7] = 0
+    q[:, 0, 0, 7] = 0x8000               # -0
+    hi[0:60, 0, 3] = inf                 # not used: a number
+    lo[20:80, 1, 5] = inf | 0x8000       # not used
+    lo[90:95, :, 7] = inf | 0x8000       # zeros alone
+    hi[90:95, :, 7] = inf
+    hi[100:110, 0, 5] = inf              # plus infinity
+    lo[110:120, 1, 3] = inf | 0x8000     # plus infinity
+    hi[120:124, :, 11] = inf             # as the query's sign there goes
+    lo[124:128, :, D - 1] = inf | 0x8000
+    lo[128, :, 5] = hi[128, :, 5] = inf | 0x8000   # minus infinity
+    table[0, :129] = np.arange(129)
+    table[1, :129] = np.arange(129)[::-1]
+    got = far.fa_kv_block_scores(dev_bits(q, dtype), dev_bits(lo, dtype), dev_bits(hi, dtype), cuda(table), cuda(lens),
+                                 check_status=True).cpu().numpy().astype(np.float64)
+    args = [widen(x, dtype) for x in (q, lo, hi)]
+    with np.errstate(invalid="ignore"):
+        want = oracle.block_scores(*args, table, lens)
+    assert not np.isnan(want).any() and np.isfinite(want[0, 0, :60]).all() and np.isposinf(want[0, 0, 100:110]).all()
+    fin = np.isfinite(want)
+    assert np.array_equal(got[~fin], want[~fin])
+    # |got - want| as for finite bounds: the sum of the terms' magnitudes, those of an unused infinite bound left out
+    a = [np.where(np.isfinite(x), x, 0.0) for x in args]
+    m = np.maximum(np.abs(a[1]), np.abs(a[2]))
+    big = oracle.block_scores(np.abs(a[0]), -m, m, table, lens)
+    assert (np.abs(got[fin] - want[fin]) <= (2 * D + 2) * 2.0 ** -23 * big[fin]).all()
+
+
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_scores_of_a_mixture_of_nan_and_infinite_bounds(Nq):
+    q, lo, hi, table, lens, _, _ = score_case(200 + Nq, 1, Nq, 8, 2, 128, 140, 140, [140 * 64])
+    table[0] = np.arange(140)
+    lo[5, 0, 9] = hi[5, 0, 9] = 0x7FC0
+    lo[6, 1, 9] = 0x7FC0                            # a NaN in one bound is enough, whatever the query's sign
+    hi[7, :, 4], lo[8, :, 4] = 0x7F80, 0xFF80
+    q[0, -1, 2, 20] = 0x7FC0                        # a NaN query vector of head 2: KV head 0
+    args = [widen(x, "bf16") for x in (q, lo, hi)]
+    with np.errstate(invalid="ignore"):
+        want = oracle.block_scores(*args, table, lens)
+    got = far.fa_kv_block_scores(dev_bits(q, "bf16"), dev_bits(lo, "bf16"), dev_bits(hi, "bf16"), cuda(table), cuda(lens),
+                                 check_status=True).cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isnan(want[0, 0]).all() and np.isnan(want[0, 1, 6])
+    fin = ~np.isnan(want)
+    assert np.array_equal(np.isinf(got[fin]), np.isinf(want[fin]))
+
+
+def test_a_block_with_a_key_beyond_f16_is_chosen():
+    # INT8 codes whose value passes 65504: the f16 bound is infinite, and a query that points away from
+    # that key still ranks the block by its other keys
+    P, D = 12, 64
+    kd = torch.ones((P * 64, 1, D), dtype=torch.int8, device="cuda")
+    ks = torch.full((P, 1, 64), 0.25, dtype=torch.float16, device="cuda")
+    kd[5 * 64 + 3, 0, 0], ks[5, 0, 3] = 127, 600.0
+    kd[5 * 64 + 9, 0, 1] = 100
+    pages = torch.arange(P, dtype=torch.int32, device="cuda")
+    lo, hi = (torch.zeros((P, 1, D), dtype=torch.float16, device="cuda") for _ in range(2))
+    far.fa_kv_block_bounds(kd, pages, None, lo, hi, k_scale=ks)
+    assert torch.isposinf(hi[5, 0, 0]) and torch.isfinite(lo).all()
+    q = torch.zeros((1, 1, 1, D), dtype=torch.float16, device="cuda")
+    q[0, 0, 0, 0], q[0, 0, 0, 1] = -1.0, 1.0
+    n = torch.tensor([P * 64], dtype=torch.int32, device="cuda")
+    sc = far.fa_kv_block_scores(q, lo, hi, pages[None], n)
+    assert sc[0, 0, 5] == 600.0 - 0.25 and (sc[0, 0, :5] == 0).all()
+    rows, _ = far.fa_kv_block_rows(sc, pages[None], n, 0, 0, 1)
+    assert rows[0, 0, 0] == 5 * 64

@@ -81,3 +81,24 @@ def test_block_rows_by_hand():
     assert n.tolist() == [[131]] and rows[0, 0, :131].tolist() == want and (rows[0, 0, 131:] == -1).all()
     rows, n = oracle.block_rows(score, np.array([[7, 2, 0, 5, 1]], np.int32), np.array([64 * 4 + 3], np.int32), 0, 0, 2, 128)
     assert n.tolist() == [[67]] and rows[0, 0, 64:67].tolist() == [64, 65, 66]   # blocks 1 and 4: the tie goes to 1
+
+
+def test_block_scores_use_the_bound_of_each_sign_alone():
+    inf = np.inf
+    q = np.array([[[[-1.0, 1.0, 0.0]]]])
+    table, n = np.array([[0]], np.int32), np.array([64], np.int32)
+
+    def score(lo, hi):
+        return oracle.block_scores(q, np.array([[lo]], float), np.array([[hi]], float), table, n)[0, 0, 0]
+    assert score([-2, -1, -1], [3, 4, 1]) == 6.0
+    assert score([-2, -inf, -inf], [inf, 4, inf]) == 6.0          # bounds that no component uses
+    assert score([-inf, -1, -1], [3, 4, 1]) == inf and score([-2, -1, -1], [3, inf, 1]) == inf
+    assert score([inf, -1, -1], [inf, 4, 1]) == -inf              # every key infinite where q is negative
+    assert np.isnan(score([inf, inf, -1], [inf, inf, 1]))         # -inf and inf meet
+    assert np.isnan(score([-2, np.nan, -1], [3, 4, 1])) and np.isnan(score([np.nan, 1, 1], [np.nan, 1, 1]))
+    # a key beyond f16 has the bound inf, and none of its products exceeds the score
+    k = np.full((64, 1, 3), 0.5)
+    k[9, 0, 0] = 127 * 600.0
+    lo, hi = (oracle.widen(b, "f16") for b in oracle.block_bounds(k, [0], None, *np.zeros((2, 1, 1, 3), np.uint16), "f16"))
+    assert hi[0, 0, 0] == inf
+    assert (k[:, 0] @ q[0, 0, 0]).max() <= oracle.block_scores(q, lo, hi, table, n)[0, 0, 0] == 0.0
