@@ -219,6 +219,9 @@ fa_status fa_rows_prefill(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_s
  * j <= kv_len[s, g] - Nq + i of its head's list, so each list must end with the
  * slice's Nq newest positions.  n_valid_hint counts the entries of all lists
  * divided by Hkv.  fa_rows_validate takes these lists with S * Hkv slices.
+ * Prefill, bf16 pools: a KV tile of two contiguous 64-row runs (blocks) counts
+ * as contiguous where fa_rows_prefill chooses between f16 and bf16 V, so lists
+ * of whole blocks take f16 V and one f16 P.
  * Sparse attention over selected blocks (the v100llm article, section 5, and
  * the llama.cpp-v100 README's QSA attend to a selected subset of the context).
  */

@@ -187,3 +187,48 @@ def test_workload_prefill_full_size_sampled_rows():
         ref, ref_lse = oracle_for(p, query_rows=rows, slices=sl)
         assert_parity(out[sl][:, rows], ref, f"prefill full slice {sl}")
         assert_lse(lse[sl][:, rows], ref_lse, f"prefill full slice {sl}")
+
+
+def _page_lists(seed, S, L, R, run=64):
+    """Lists of whole 64-row pages wherever they lie, the last one cut."""
+    g = synth.rng(seed)
+    starts = np.stack([g.permutation(R // run)[: -(-L // run)] * run for _ in range(S)])
+    return (starts[:, :, None] + np.arange(run)).reshape(S, -1)[:, :L].astype(np.int32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("L,Nq,Hq,Hkv,hole", [(1000, 130, 8, 2, False), (640, 64, 4, 4, True), (64, 10, 8, 1, False),
+                                             (129, 200, 16, 2, False)])
+def test_prefill_over_scattered_pages(L, Nq, Hq, Hkv, hole, dtype):
+    p = synth.random_problem(40 + L, S=2, Nq=Nq, Hq=Hq, Hkv=Hkv, D=128, R=4096, L=L, causal=L >= Nq, pad_frac=0.0,
+                             dtype=dtype)
+    p.kv_rows = _page_lists(41, 2, L, 4096)
+    if hole:
+        p.kv_rows[0, 70], p.kv_rows[1, :3] = -1, -1
+    out, lse = run_prefill(p)
+    ref, ref_lse = oracle_for(p)
+    assert_parity(out, ref, "pages")
+    assert_lse(lse, ref_lse, "pages")
+
+
+@pytest.mark.parametrize("run", [64, 1])
+def test_bf16_prefill_over_pages_keeps_sixteen_bits_of_p(run):
+    """All P but the first are r = 0.5 + 2^-12 - 2^-16, which one f16 rounds to 0.5, and V is 1.
+
+    The output is the sum of the rounded P over the sum of P: 1 - 2^-11 * 15/16 with one f16 P, 1 with the pair
+    (rn8(r) = 0.5 leaves 15 * 2^-16, a bf16 value).  Beside that: r comes from an exponential that is off by less
+    than 2^-20 of itself, which the pair rounds to within 2^-9 of the rest, at most 2^-21; L / 16 = 60 sums of 16
+    in the tensor core, each cut off at 2^-23: 2^-17.  Together below 2^-16.
+    """
+    L, Nq = 960, 60
+    k = np.zeros((4096, 1, 128), np.float32)
+    rows = _page_lists(43, 1, L, 4096, run)
+    k[:, 0, 0] = -1.0
+    k[rows[0, 0], 0, 0] = 0.0
+    kb, vb, qb = (synth.f32_to_bf16_bits(x) for x in (k, np.ones_like(k), np.full((1, Nq, 1, 128), 1.0, np.float32)))
+    scale = -float(np.log(0.5 + 2.0 ** -12 - 2.0 ** -16))
+    out, lse = far.fa_rows_prefill(dev_bits(qb, "bf16"), dev_bits(kb, "bf16"), dev_bits(vb, "bf16"),
+                                   torch.from_numpy(rows).cuda(), scale, want_lse=True)
+    assert (out - 1).abs().max() < 2.0 ** -16, (out - 1).abs().max()
+    want = np.log(1 + (L - 1) * (0.5 + 2.0 ** -12 - 2.0 ** -16))
+    assert np.allclose(lse.cpu().numpy(), want, rtol=0, atol=1e-5)
