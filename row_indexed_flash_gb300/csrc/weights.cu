@@ -107,11 +107,19 @@ __global__ void __launch_bounds__(kWKeys) weights_generic_kernel(const WeightsPa
   }
 }
 
+constexpr int kWMaxD = 256;
+constexpr size_t weights_smem(int D) { return ((size_t)kWKeys * (D + 1) + kWVec * D + kWVec) * sizeof(float); }
+
 template <int KIND>
 cudaError_t weights_generic(const WeightsParams& p, cudaStream_t st) {
-  const size_t smem = ((size_t)kWKeys * (p.D + 1) + kWVec * p.D + kWVec) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(weights_generic_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  if (p.D > kWMaxD) return cudaErrorInvalidValue;
+  const size_t smem = weights_smem(p.D);
+  // the limit of the largest call, once: the attribute is the device's, and
+  // another thread's call may lie between its setting and this launch
+  const cudaError_t e = once_per_device<5>([] {
+    return cudaFuncSetAttribute(weights_generic_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)weights_smem(kWMaxD));
+  });
   if (e != cudaSuccess) return e;
   const dim3 grid((p.L + kWKeys - 1) / kWKeys, p.Hkv, p.S);
   weights_generic_kernel<KIND><<<grid, kWKeys, smem, st>>>(p);

@@ -6,6 +6,8 @@ most e = (D + 8) * 2^-23 * scale * sum_d |q_d k_d| + 2^-22 * (|x| + |lse| + 1)
 2^-23 a step, since the tensor core's sums need not round to nearest), the
 hardware exponential 2^-21, and the sum of nv terms nv * 2^-24 of itself.
 """
+import ctypes
+import threading
 import time
 
 import numpy as np
@@ -322,3 +324,37 @@ def test_an_expired_wait_leaves_no_copy_behind(Nq, G, L):
         far.fa_set_wait_limit_ns(0)
     assert torch.equal(far.fa_rows_weights(q, kd, rows, p.scale, lse, workspace=ws, check_status=True), want)
     assert max(spent) < 0.5, spent
+
+
+def test_weights_of_several_head_dims_from_several_threads():
+    """Calls of one kernel that need unequal amounts of shared memory, at the same time."""
+    cases = []
+    for D in (256, 96, 32, 224):
+        p, kd, _, _ = make(380 + D, S=1, Nq=2, Hq=4, Hkv=2, D=D, R=512, L=130, with_mask=True)
+        q, rows, mask = dev_bits(p.q, "bf16"), torch.from_numpy(p.kv_rows).cuda(), torch.from_numpy(p.mask).cuda()
+        lse = torch.zeros((1, 2, 4), device="cuda")
+        acc, ws = torch.zeros((1, 2, 130), device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        want = far.fa_rows_weights(q, kd, rows, 0.05, lse, mask=mask, decay=0.0)
+        a, out, _ = far.make_args(q, kd, kd, rows, 0.05, mask=mask)
+        args = (ctypes.byref(a), lse.data_ptr(), 0.0, acc.data_ptr(), ws.data_ptr(), 256, stream.cuda_stream)
+        cases.append((D, args, acc, want, (q, kd, rows, mask, lse, ws, out, a, stream)))
+    torch.cuda.synchronize()
+    call, wrong = far.lib().fa_rows_weights, []
+
+    def work(D, args):
+        for _ in range(4000):
+            if call(*args):
+                wrong.append((D, far.fa_last_error()))
+                return
+
+    threads = [threading.Thread(target=work, args=c[:2], daemon=True) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+        assert not t.is_alive()
+    torch.cuda.synchronize()
+    assert not wrong, wrong[:3]
+    for D, _, acc, want, _ in cases:
+        assert torch.equal(acc, want), D
