@@ -318,6 +318,8 @@ def fa_rows_decode_heads(q, k, v, kv_rows, scale, **kw):
     Keyword args as fa_rows_decode, without mask; n_valid_hint is the entries of
     all lists divided by Hkv.
     """
+    _check_scale(k, kw.get("k_scale"))
+    _check_scale(v, kw.get("v_scale"), "v_scale")
     _same_device(q.device, k, v, kv_rows, *(kw.get(x) for x in _ATTEND_TENSORS))
     with _on(q.device):
         return _attend("fa_rows_decode_heads", False, q, k, v, kv_rows, scale, head_lists=True, **kw)
@@ -480,12 +482,12 @@ def fa_kv_block_bounds(k, pages, fill, kmin, kmax, *, k_scale=None, stream=None)
     return kmin, kmax
 
 
-def _check_scale(k, k_scale):
-    if k.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
-        if k_scale is None:
-            raise ValueError("a quantised pool needs k_scale")
-        if k_scale.element_size() != 2 or k_scale.numel() != k.shape[0] * k.shape[1]:
-            raise ValueError("k_scale must be fp16 [R/64, Hkv, 64]")
+def _check_scale(pool, scale, name="k_scale"):
+    if pool.dtype in (torch.int8, torch.uint8, torch.float8_e4m3fn):
+        if scale is None:
+            raise ValueError(f"a quantised pool needs {name}")
+        if scale.dtype != torch.float16 or scale.shape != (pool.shape[0] // 64, pool.shape[1], 64):
+            raise ValueError(f"{name} must be float16 [R/64, Hkv, 64]")
 
 
 def _check_pages(S, page_table, seq_len, slice_seq):

@@ -108,3 +108,31 @@ def test_binding_refuses_scales_of_another_pool():
             far.fa_rows_weights(q, k, rows, 1.0, torch.zeros((1, 1, 4)), k_scale=ks)
         with pytest.raises(ValueError, match="k_scale"):
             far.fa_kv_block_bounds(k, rows[0], None, bound, bound.clone(), k_scale=ks)
+
+
+@pytest.mark.parametrize("ks", [
+    torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.zeros((2, 2, 64), dtype=torch.int16),
+    torch.zeros((128, 2), dtype=torch.float16), torch.zeros((2, 64, 2), dtype=torch.float16),
+    torch.zeros((1, 4, 64), dtype=torch.float16), torch.zeros(256, dtype=torch.float16)])
+def test_binding_refuses_scales_of_another_type_or_layout(ks):
+    q = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16)
+    rows = torch.zeros((1, 8), dtype=torch.int32)
+    bound = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    for k in (torch.zeros((128, 2, 64), dtype=torch.int8), torch.zeros((128, 2, 32), dtype=torch.uint8),
+              torch.zeros((128, 2, 64), dtype=torch.float8_e4m3fn)):
+        with pytest.raises(ValueError, match="k_scale"):
+            far.fa_rows_weights(q, k, rows, 1.0, torch.zeros((1, 1, 4)), k_scale=ks)
+        with pytest.raises(ValueError, match="k_scale"):
+            far.fa_kv_block_bounds(k, rows[0], None, bound, bound.clone(), k_scale=ks)
+        fine = torch.zeros((2, 2, 64), dtype=torch.float16)
+        for kw in (dict(k_scale=ks, v_scale=fine), dict(k_scale=fine, v_scale=ks)):
+            with pytest.raises(ValueError, match="float16"):
+                far.fa_rows_decode_heads(q, k, k, rows[None], 1.0, **kw)
+
+
+def test_binding_takes_scales_of_the_pool():
+    # past the shape checks: refused for being on the host
+    k, ks = torch.zeros((128, 2, 64), dtype=torch.int8), torch.zeros((2, 2, 64), dtype=torch.float16)
+    bound = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        far.fa_kv_block_bounds(k, torch.zeros(1, dtype=torch.int32), None, bound, bound.clone(), k_scale=ks)
