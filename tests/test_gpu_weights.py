@@ -358,3 +358,36 @@ def test_weights_of_several_head_dims_from_several_threads():
     assert not wrong, wrong[:3]
     for D, _, acc, want, _ in cases:
         assert torch.equal(acc, want), D
+
+
+@pytest.mark.parametrize("kv,dtype", [("bf16", "bf16"), ("f16", "f16"), ("i8", "bf16"), ("i4", "f16"), ("f8", "bf16")])
+@pytest.mark.parametrize("Nq,Hq,Hkv,D,L,causal", [
+    (1, 8, 2, 128, 3000, False), (1, 64, 2, 64, 700, False), (16, 8, 2, 256, 1111, True), (128, 4, 4, 128, 900, True),
+    (129, 4, 4, 128, 900, True), (2048, 8, 2, 128, 16384, True), (2048, 8, 1, 256, 2500, True), (1500, 14, 2, 64, 1700, True),
+    (901, 10, 2, 128, 1000, True), (300, 128, 1, 128, 600, True), (77, 64, 1, 256, 513, False), (40, 8, 2, 96, 333, True)])
+def test_weights_of_equal_terms_count_the_queries(Nq, Hq, Hkv, D, L, causal, kv, dtype):
+    """Keys of zero and lse of zero: each term is exp(0) = 1, so an entry's weight is the number of (query, head)
+    pairs that see it, exactly: no query vector, tile or limit may be lost or taken twice."""
+    R = -(-L // 64) * 64
+    g = synth.rng(390 + L)
+    q = dev_bits(synth.normal_bits(g, (2, Nq, Hq, D), dtype), dtype)
+    kd = {"i4": torch.zeros((R, Hkv, D // 2), dtype=torch.uint8), "i8": torch.zeros((R, Hkv, D), dtype=torch.int8),
+          "f8": torch.zeros((R, Hkv, D), dtype=torch.uint8).view(torch.float8_e4m3fn)}.get(
+              kv, torch.zeros((R, Hkv, D), dtype=q.dtype)).cuda()
+    ks = torch.ones((R // 64, Hkv, 64), dtype=torch.float16, device="cuda") if kv in QUANT else None
+    rows = torch.from_numpy(np.stack([g.permutation(R)[:L] for _ in range(2)]).astype(np.int32)).cuda()
+    rows[0, L // 3] = -1
+    lens = torch.tensor([L, L - L // 5], dtype=torch.int32, device="cuda")
+    lse = torch.zeros((2, Nq, Hq), device="cuda")
+    lse[1, Nq // 2] = -float("inf")                       # a query that saw nothing
+    got = far.fa_rows_weights(q, kd, rows, 0.3, lse, kv_len=lens, causal=causal, k_scale=ks, check_status=True)
+    j, i = torch.arange(L, device="cuda"), torch.arange(Nq, device="cuda")
+    want = torch.zeros((2, L), device="cuda")
+    for s, n in enumerate(lens.tolist()):
+        see = ((rows[s] >= 0) & (j < n))[None].repeat(Nq, 1)
+        if causal:
+            see &= j[None] <= n - Nq + i[:, None]
+        if s == 1:
+            see &= (i != Nq // 2)[:, None]
+        want[s] = see.sum(0) * (Hq // Hkv)
+    assert torch.equal(got, want[:, None].expand(2, Hkv, L))
