@@ -47,19 +47,6 @@ int next_pow2(int x) {
   return p;
 }
 
-// SM count of the current device, cached per device once it has been read
-// (a failed query is not cached: it answers 1 and is retried next time).
-int sm_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 1;
-  cached[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 int kv_kind(fa_dtype d) {
   switch (d) {
     case FA_BF16: return far::KV_BF16;
@@ -199,7 +186,7 @@ fa_status plan_decode(const fa_rows_args* a, DecodePlan* pl) {
   else if (kind == far::KV_F16) occ = far::decode_occupancy_f16(a->D, qvp);
   else if (kind == far::KV_I8) occ = far::decode_occupancy_i8(a->D, qvp);
   if (occ <= 0) return fail(FA_ERR_CUDA, "decode kernel cannot be resident (no device, or shared memory too small)");
-  const long long slots = (long long)sm_count() * occ;
+  const long long slots = (long long)far::sm_count() * occ;
   const long long units = (long long)a->S * a->Hkv;
   const bool ragged = a->n_valid_hint > 0;
   const double lavg = ragged ? (double)a->n_valid_hint / a->S : (double)L;
@@ -726,7 +713,7 @@ fa_status fa_kv_evict(const float* acc, const int32_t* kv_rows, const int32_t* k
   p.recent = recent;
   p.k = k;
   p.out_len = out_len;
-  cudaError_t e = far::evict_launch(p, sm_count(), reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = far::evict_launch(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, "evict launch");
 }
 

@@ -437,15 +437,16 @@ namespace far {
 template <int D, int QVP, int KIND>
 int decode_occupancy_inst() {
   using Sh = DecodeShape<D, QVP, KIND>;
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (cached[dev] > 0) return cached[dev];
+  const int c = cached[dev].load(std::memory_order_relaxed);
+  if (c > 0) return c;
   auto kern = fa_rows_decode_kernel<D, QVP, KIND>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) != cudaSuccess) return 0;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, Sh::NW * 32, Sh::SMEM) != cudaSuccess) return 0;
-  cached[dev] = n;
+  cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -749,10 +749,11 @@ bool dk_map(CUtensorMap* m, const void* base, bool bf16, int D, int Hkv, long lo
 
 template <int D, int QVP, int KQ, int NS>
 int dk_occupancy() {
-  static int cached[64] = {0};
+  static std::atomic<int> cached[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (cached[dev] > 0) return cached[dev];
+  const int c = cached[dev].load(std::memory_order_relaxed);
+  if (c > 0) return c;
   using Sh = DkShape<D, QVP, KQ, NS>;
   auto kern = fa_rows_decode_tc_kernel<D, QVP, KQ, NS>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM) != cudaSuccess) return 0;
@@ -761,7 +762,7 @@ int dk_occupancy() {
   // tensor memory also bounds residency: 512 columns per SM
   const int by_tmem = 512 / (int)Sh::TMEM_COLS;
   n = n < by_tmem ? n : by_tmem;
-  cached[dev] = n;
+  cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

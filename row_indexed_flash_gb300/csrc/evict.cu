@@ -322,11 +322,11 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_kernel(const EvictParams 
 
 }  // namespace
 
-cudaError_t evict_launch(const EvictParams& p, int sm_count, cudaStream_t st) {
+cudaError_t evict_launch(const EvictParams& p, cudaStream_t st) {
   // CTAs per slice: enough for about 2048 positions each, no more than the
   // SMs there are for all slices
   int C = 1;
-  while (C < kEvMaxCluster && p.L > C * 2048 && (long long)p.S * C * 2 <= sm_count) C *= 2;
+  while (C < kEvMaxCluster && p.L > C * 2048 && (long long)p.S * C * 2 <= sm_count()) C *= 2;
   const int chunk = ((p.L + C - 1) / C + 31) & ~31;
   const int cap = chunk < kEvCap ? chunk : kEvCap;
   const cudaError_t e = once_per_device<0>([] {

@@ -16,6 +16,6 @@ struct EvictParams {
   int32_t* freed;   // NULL: not wanted
   int S, Hkv, L, sinks, recent, k, out_len;
 };
-cudaError_t evict_launch(const EvictParams& p, int sm_count, cudaStream_t st);
+cudaError_t evict_launch(const EvictParams& p, cudaStream_t st);
 
 }  // namespace far

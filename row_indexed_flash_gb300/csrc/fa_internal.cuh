@@ -151,6 +151,19 @@ cudaError_t launch_sparse_rows_ws(const float* score, int n_max, const int32_t* 
 cudaError_t launch_validate(const int32_t* rows, const int32_t* kv_len, int S, int L, long long R,
                             long long* status, cudaStream_t st);
 
+// SM count of the current device, cached per device once it has been read
+// (a failed query is not cached: it answers 1 and is retried next time).
+inline int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 1;
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // Runs f (which returns a cudaError_t, such as the setting of a kernel's
 // attributes) once per device and place in the code; repeated until it succeeds.
 template <int PLACE, class F>

@@ -1478,15 +1478,6 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
 // ---------------------------------------------------------------------------
 // host side
 
-int ks_sms() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (cached[dev] == 0 && cudaDeviceGetAttribute(&cached[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cached[dev] = 0;
-  return cached[dev] > 0 ? cached[dev] : 1;
-}
-
 bool ks_map(CUtensorMap* m, const void* base, bool bf16, int D, int Hkv, long long R) {
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)R};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * Hkv * 2};
@@ -1515,7 +1506,7 @@ cudaError_t ks_stream(const KeyScanParams& p, cudaStream_t st) {
     if (MODE == SCAN_SCORES && !ks_map(&t1, p.k[1], p.q_bf16 != 0, D, p.Hkv, p.R)) return cudaErrorInvalidValue;
   }
   const long long most = (long long)p.S * p.Hkv * ((p.L + ks::BM - 1) / ks::BM);
-  const int sms = ks_sms();
+  const int sms = sm_count();
   const int grid = (int)(most < sms ? most : sms);
   kern<<<grid, ks::kThreads<QUANT>, ly.total, st>>>(p, tma, t0, t1);
   return cudaGetLastError();
@@ -1535,7 +1526,7 @@ cudaError_t ks_prompt(const KeyScanParams& p, cudaStream_t st) {
   pl.sc = 1;
   const int tiles = (p.L + ks::BM - 1) / ks::BM;
   pl.tiles = tiles;
-  const long long slots = ks_sms();
+  const long long slots = sm_count();
   if (MODE == SCAN_WEIGHTS) {
     pl.PT = Sh::N / p.G;
     const long long queries = (long long)p.S * p.Nq;

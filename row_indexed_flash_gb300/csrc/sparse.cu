@@ -483,14 +483,10 @@ cudaError_t launch_sparse_rows_ws(const float* score, int n_max, const int32_t* 
 cudaError_t launch_sparse_rows(const float* score, int n_max, const int32_t* n_len, int S, int sinks, int recent, int k,
                                const int32_t* row_map, int32_t* rows, int list_len, cudaStream_t st) {
   if (S == 0) return cudaSuccess;
-  static int attr_set[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (!attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(sparse_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSelSmem);
-    if (e != cudaSuccess) return e;
-    attr_set[dev] = 1;
-  }
+  const cudaError_t e = once_per_device<6>([] {
+    return cudaFuncSetAttribute(sparse_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSelSmem);
+  });
+  if (e != cudaSuccess) return e;
   sparse_rows_kernel<<<S, kSelThreads, kSelSmem, st>>>(score, n_max, n_len, sinks, recent, k, row_map, rows, list_len);
   return cudaGetLastError();
 }

@@ -1,6 +1,7 @@
 """The C-ABI library loads and exports every entry point its header declares;
 host-side argument checks reject bad calls before anything is launched (CPU)."""
 import ctypes
+import glob
 import os
 import re
 
@@ -122,3 +123,19 @@ def test_every_workspace_starts_with_the_status_block(lib):
     assert lib.fa_rows_workspace_size(ctypes.byref(a), 1) == 256      # prefill: the status block
     st = lib.fa_rows_prefill(ctypes.byref(a), None, 0, None)
     assert st == 3 and "status word" in far.fa_last_error()           # refused before anything is launched
+
+
+def test_what_host_threads_share_is_atomic_or_locked():
+    """Function-local and file-level state of the launch code: calls may come from several threads."""
+    csrc = os.path.join(os.path.dirname(far.__file__), "csrc")
+    found = []
+    for path in glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh")):
+        text = open(path).read()
+        locked = "std::lock_guard" in text or "std::call_once" in text
+        for line in text.splitlines():
+            m = re.match(r"\s*(?:static|thread_local)\s+((?:std::)?[\w:<>*]+)\s+\w+\s*(?:\[[^\]]*\])?\s*(?:=[^;]*|\{[^;]*)?;", line)
+            if m and not line.strip().startswith("thread_local") and m.group(1) not in ("constexpr", "const"):
+                atomic = m.group(1).startswith(("std::atomic", "std::mutex", "std::once_flag"))
+                if not (atomic or locked):
+                    found.append((os.path.basename(path), line.strip()))
+    assert not found, found
