@@ -130,6 +130,20 @@ def test_binding_refuses_scales_of_another_type_or_layout(ks):
                 far.fa_rows_decode_heads(q, k, k, rows[None], 1.0, **kw)
 
 
+def test_binding_finds_the_current_stream_by_the_public_interface_too(monkeypatch):
+    class Stream:
+        cuda_stream = 4711
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: asked.append(device) or Stream())
+    monkeypatch.setattr(far, "_raw_stream", None)      # a torch without the private function
+    for device in (torch.device("cuda", 1), torch.device("cuda")):
+        assert far._stream(None, device) == 4711
+    assert asked == [torch.device("cuda", 1), torch.device("cuda")]
+    monkeypatch.setattr(far, "_raw_stream", lambda index: 100 + index)
+    assert far._stream(None, torch.device("cuda", 1)) == 101 and far._stream(None, torch.device("cuda")) == 4711
+    assert far._stream(Stream(), torch.device("cuda", 1)) == 4711 and far._stream(12, torch.device("cuda", 1)) == 12
+
+
 def test_binding_takes_scales_of_the_pool():
     # past the shape checks: refused for being on the host
     k, ks = torch.zeros((128, 2, 64), dtype=torch.int8), torch.zeros((2, 2, 64), dtype=torch.float16)

@@ -485,3 +485,14 @@ def test_a_block_with_a_key_beyond_f16_is_chosen():
     assert sc[0, 0, 5] == 600.0 - 0.25 and (sc[0, 0, :5] == 0).all()
     rows, _ = far.fa_kv_block_rows(sc, pages[None], n, 0, 0, 1)
     assert rows[0, 0, 0] == 5 * 64
+
+
+def test_current_stream_is_the_same_by_both_interfaces(monkeypatch):
+    side = torch.cuda.Stream()
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            fast = far._stream(None, dev)
+            with monkeypatch.context() as m:
+                m.setattr(far, "_raw_stream", None)
+                assert far._stream(None, dev) == fast == stream.cuda_stream
