@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
       for (int j = 0; j < T; ++j) {
         const int st = j % NST, u = j / NST;
         if (!__all_sync(0xffffffffu, mbar_wait(empty + st, (u & 1) ^ 1, abort_flag, wait_ns))) break;
+        tma_pend &= ~(1u << st);
         int rows[2] = {nrow0, nrow1};
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -541,7 +542,9 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
         cp_async_mbar_arrive_noinc(full + st);
       }
       cp_async_wait_all();
-      if (gw == 0 && lane == 0 && *abort_flag) {   // no TMA load may still be writing when the CTA exits
+      // No TMA load may still be writing when the CTA exits.  Waited for whether or
+      // not a wait has run out: one may run out after this warp has issued its last.
+      if (gw == 0 && lane == 0) {
         for (int c = 0; c < NST; ++c)
           if ((tma_pend >> c) & 1u) wait_drain(full + c, (tma_par >> c) & 1u);
       }

@@ -402,6 +402,7 @@ __global__ void __maxnreg__((DqShape<QVP, KQ>::MAXREG))
         nx2[t] = entry_raw((j + 2) * BN + lane + 32 * t);
       }
       if (!__all_sync(0xffffffffu, mbar_wait(pv_done + c, (u & 1) ^ 1, abort_flag, wait_ns))) break;
+      tma_pend &= ~(1u << c);
       unsigned char* Kc = sm + Sh::OFF_C + c * Sh::STAGE;
       unsigned char* Vc = Kc + Sh::VATOM;
       // half h holds entries 64h .. 64h + 63 (lane values r[2h], r[2h + 1]);
@@ -453,7 +454,9 @@ __global__ void __maxnreg__((DqShape<QVP, KQ>::MAXREG))
       }
     }
     cp_async_wait_all();
-    if (lane == 0 && *abort_flag) {   // no TMA load may still be writing when the CTA exits
+    // No TMA load may still be writing when the CTA exits.  Waited for whether or
+    // not a wait has run out: one may run out after this warp has issued its last.
+    if (lane == 0) {
       for (int c = 0; c < NC; ++c)
         if ((tma_pend >> c) & 1u) dq_wait_drain(code_full + c, (tma_par >> c) & 1u);
     }

@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(pf::NWARP * 32, 1)
         }
       }
       cp_async_wait_all();
-      // bulk copies still in flight must land before the CTA can exit
-      if (lead && *abort_flag) {
+      // Bulk copies still in flight must land before the CTA can exit.  Waited for
+      // whether or not a wait has run out: one may run out after the last is issued.
+      if (lead) {
         if (q_pending) mbar_wait_drain(q_full, 0);
         for (int st = 0; st < NST; ++st) {
           if ((tma_pend >> st) & 1u) mbar_wait_drain(k_full + st, (tma_par >> st) & 1u);

@@ -129,3 +129,35 @@ def test_prefill_refuses_a_missing_workspace():
     import ctypes
     st = far.lib().fa_rows_prefill(ctypes.byref(a), None, 0, torch.cuda.current_stream().cuda_stream)
     assert st == 3 and "status word" in far.fa_last_error()
+
+
+@pytest.mark.parametrize("L", [64, 128, 192, 1000])
+@pytest.mark.parametrize("kind", ["decode_bf16", "decode_int8", "prefill_bf16"])
+def test_expired_waits_over_pages_leave_no_copy_behind(kind, L):
+    """Lists of whole pages, whose tiles are copied by TMA: with few of them every copy is issued without a wait,
+    and whether one must be drained shows only after the roles that wait for it have given up."""
+    p = synth.random_problem(910 + L, S=2, Nq=2, Hq=8, Hkv=2, D=128, R=4096, L=L, pad_frac=0.0)
+    starts = np.stack([synth.rng(911 + s).permutation(64)[: -(-L // 64)] * 64 for s in range(2)])
+    p.kv_rows = (starts[:, :, None] + np.arange(64)).reshape(2, -1)[:, :L].astype(np.int32)
+    q, k, v = (dev_bits(x, "bf16") for x in (p.q, p.k, p.v))
+    rows, kw = torch.from_numpy(p.kv_rows).cuda(), {}
+    if kind == "decode_int8":
+        (k, ks), (v, vs) = (far.fa_kv_quantize_int8(x, p.R) for x in (k, v))
+        kw = dict(k_scale=ks, v_scale=vs)
+    fn = far.fa_rows_prefill if kind == "prefill_bf16" else far.fa_rows_decode
+    ws = torch.zeros(4 << 20, dtype=torch.uint8, device="cuda")
+
+    def call():
+        return fn(q, k, v, rows, p.scale, want_lse=True, workspace=ws, **kw)
+
+    out, lse = call()
+    assert far.fa_rows_status(ws) == 0
+    try:
+        for limit in (1, 1, 500, 2000):
+            far.fa_set_wait_limit_ns(limit)
+            call()
+            assert far.fa_rows_status(ws, clear=True) & ~far.FA_WS_WAIT_EXPIRED == 0
+    finally:
+        far.fa_set_wait_limit_ns(0)
+    again, lse2 = call()
+    assert far.fa_rows_status(ws) == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
