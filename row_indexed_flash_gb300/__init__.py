@@ -167,6 +167,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _stream(stream, device) -> int:
     if stream is None:
         if _raw_stream is not None and device.index is not None:
@@ -175,17 +178,35 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made_for(stream, device):
+    """Context in which a call's new tensors are made: they belong to the stream that the call works on,
+    so that they are zeroed before its kernels run and not handed out again while these still use them."""
+    if stream is None:
+        return _NOTHING
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream, device), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _new(make, shape, dtype, device, stream):
+    """A new tensor (make: torch.empty or torch.zeros) of the call's stream."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _made_for(stream, device):
+        return make(shape, dtype=dtype, device=device)
+
+
 class _Workspace:
     """Caller-side scratch (status word, split counters, partials): grown on demand, zeroed once."""
 
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
 
-    def get(self, nbytes: int, device, stream_handle: int) -> Tuple[int, int]:
+    def get(self, nbytes: int, device, stream_handle: int, stream=None) -> Tuple[int, int]:
         if nbytes == 0:
             return 0, 0
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            self.buf = _new(torch.empty, max(nbytes, 1 << 20), torch.uint8, device, stream)
             _check(lib().fa_rows_workspace_init(self.buf.data_ptr(), self.buf.numel(), stream_handle))
         return self.buf.data_ptr(), self.buf.numel()
 
@@ -208,8 +229,8 @@ def default_workspace(device=None, stream=None, is_prefill: bool = False) -> Opt
 
 
 def make_args(q, k, v, kv_rows, scale, *, kv_len=None, mask=None, causal=False, k_scale=None, v_scale=None,
-              out=None, lse=None, out_dtype=torch.float32, want_lse=False, n_valid_hint=0, head_lists=False):
-    """Builds fa_rows_args from torch tensors; allocates ``out``/``lse`` if not given.
+              out=None, lse=None, out_dtype=torch.float32, want_lse=False, n_valid_hint=0, head_lists=False, stream=None):
+    """Builds fa_rows_args from torch tensors; allocates ``out``/``lse`` (of ``stream``) if not given.
 
     head_lists: kv_rows is [S, Hkv, L] and kv_len [S, Hkv], one list per KV head.
     """
@@ -230,9 +251,9 @@ def make_args(q, k, v, kv_rows, scale, *, kv_len=None, mask=None, causal=False, 
     if mask is not None and (mask.dtype != torch.float32 or tuple(mask.shape) != (S, Nq, kv_rows.shape[-1])):
         raise ValueError("mask must be float32 [S, Nq, L]")
     if out is None:
-        out = torch.empty((S, Nq, Hq, D), dtype=out_dtype, device=q.device)
+        out = _new(torch.empty, (S, Nq, Hq, D), out_dtype, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((S, Nq, Hq), dtype=torch.float32, device=q.device)
+        lse = _new(torch.empty, (S, Nq, Hq), torch.float32, q.device, stream)
     a = fa_rows_args()
     a.q, a.q_dtype = _ptr(q), _DT[q.dtype]
     a.k, a.v, a.kv_dtype = _ptr(k), _ptr(v), _DT[k.dtype]
@@ -267,9 +288,10 @@ def fa_rows_status(ws: torch.Tensor, clear: bool = False, stream=None) -> int:
     """The workspace's status word (FA_WS_WAIT_EXPIRED set: a call on it had a
     pipeline wait run out).  Synchronises the stream to read it."""
     sh = _stream(stream, ws.device)
-    word = torch.empty(1, dtype=torch.int32, device=ws.device)
-    _check(lib().fa_rows_status(_ptr(ws), ws.numel() * ws.element_size(), word.data_ptr(), int(clear), sh))
-    return int(word.item()) & 0xffffffff
+    with _made_for(stream, ws.device):   # and read on
+        word = torch.empty(1, dtype=torch.int32, device=ws.device)
+        _check(lib().fa_rows_status(_ptr(ws), ws.numel() * ws.element_size(), word.data_ptr(), int(clear), sh))
+        return int(word.item()) & 0xffffffff
 
 
 def fa_set_wait_limit_ns(limit_ns: int):
@@ -279,12 +301,12 @@ def fa_set_wait_limit_ns(limit_ns: int):
 
 def _attend(entry: str, is_prefill: bool, q, k, v, kv_rows, scale, *, workspace=None, stream=None,
             check_status=False, **kw):
-    a, out, lse = make_args(q, k, v, kv_rows, scale, **kw)
+    a, out, lse = make_args(q, k, v, kv_rows, scale, stream=stream, **kw)
     sh = _stream(stream, q.device)
     need = fa_rows_workspace_size(a, is_prefill)
     if workspace is None:
         wsobj = _default_ws(q.device, sh, is_prefill)
-        wptr, wbytes = wsobj.get(need, q.device, sh)
+        wptr, wbytes = wsobj.get(need, q.device, sh, stream)
         wtensor = wsobj.buf
     else:
         wptr, wbytes = _ptr(workspace), workspace.numel() * workspace.element_size()
@@ -338,13 +360,13 @@ def fa_rows_prefill_heads(q, k, v, kv_rows, scale, **kw):
         return _attend("fa_rows_prefill_heads", True, q, k, v, kv_rows, scale, head_lists=True, **kw)
 
 
-def _status_ws(workspace, device, sh, need: int = 256):
+def _status_ws(workspace, device, sh, stream, need: int = 256):
     """(pointer, bytes, tensor) of the caller's workspace or the binding's own one for calls that
     need the status block alone."""
     if workspace is not None:
         return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
     wsobj = _default_ws(device, sh, True)
-    wptr, wbytes = wsobj.get(need, device, sh)
+    wptr, wbytes = wsobj.get(need, device, sh, stream)
     return wptr, wbytes, wsobj.buf
 
 
@@ -352,9 +374,6 @@ def _raise_expired(entry: str, wtensor, stream):
     word = fa_rows_status(wtensor, clear=True, stream=stream)
     if word & FA_WS_WAIT_EXPIRED:
         raise FaRowsError(FA_ERR_WAIT_EXPIRED, f"{entry}: a pipeline wait ran out; the outputs are invalid")
-
-
-_NOTHING = contextlib.nullcontext()
 
 
 def _on(device):
@@ -409,7 +428,7 @@ def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, 
     if mask is not None and (mask.dtype != torch.float32 or mask.shape != (S, Nq, L)):
         raise ValueError("mask must be float32 [S, Nq, L]")
     if acc is None:
-        acc = torch.zeros((S, Hkv, L), dtype=torch.float32, device=q.device)
+        acc = _new(torch.zeros, (S, Hkv, L), torch.float32, q.device, stream)
     elif acc.dtype != torch.float32 or acc.shape != (S, Hkv, L):
         raise ValueError("acc must be float32 [S, Hkv, L]")
     _check_scale(k, k_scale)
@@ -425,7 +444,7 @@ def fa_rows_weights(q, k, kv_rows, scale, lse, acc=None, *, decay: float = 1.0, 
     a.S, a.Nq, a.Hq, a.Hkv, a.D = S, Nq, Hq, Hkv, D
     with _on(dev):
         sh = _stream(stream, dev)
-        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh)
+        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh, stream)
         _check(lib().fa_rows_weights(ctypes.byref(a), plse, float(decay), pacc, wptr, wbytes, sh))
     if check_status:
         _raise_expired("fa_rows_weights", wtensor, stream)
@@ -451,7 +470,7 @@ def fa_kv_evict(acc, kv_rows, kv_len, sinks: int, recent: int, k: int, *, out_le
 
     def dest(t, shape, dtype, name):
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return _new(torch.empty, shape, dtype, dev, stream)
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name} must be {dtype} {shape}")
         return t
@@ -515,14 +534,14 @@ def fa_kv_block_scores(q, kmin, kmax, page_table, seq_len, *, slice_seq=None, ou
     _check_pages(S, page_table, seq_len, slice_seq)
     n_seq, max_pages = page_table.shape
     if out is None:
-        out = torch.empty((S, Hkv, max_pages), dtype=torch.float32, device=q.device)
+        out = _new(torch.empty, (S, Hkv, max_pages), torch.float32, q.device, stream)
     elif out.dtype != torch.float32 or out.shape != (S, Hkv, max_pages):
         raise ValueError("out must be float32 [S, Hkv, max_pages]")
     dev = q.device
     pq, plo, phi, pt, pn, pseq, po, _ = _ptrs(dev, q, kmin, kmax, page_table, seq_len, slice_seq, out, workspace)
     with _on(dev):
         sh = _stream(stream, dev)
-        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh)
+        wptr, wbytes, wtensor = _status_ws(workspace, dev, sh, stream)
         _check(lib().fa_kv_block_scores(pq, _DT[q.dtype], S, Nq, Hq, Hkv, D, plo, phi, P, pt, n_seq, max_pages, pn,
                                         pseq, po, wptr, wbytes, sh))
     if check_status:
@@ -542,11 +561,11 @@ def fa_kv_block_rows(score, page_table, seq_len, sink_blocks: int, recent_blocks
         raise ValueError("page_table and score must have the same max_pages")
     L = 64 * (int(sink_blocks) + int(recent_blocks) + int(k)) if list_len is None else int(list_len)
     if out is None:
-        out = torch.empty((S, Hkv, L), dtype=torch.int32, device=score.device)
+        out = _new(torch.empty, (S, Hkv, L), torch.int32, score.device, stream)
     elif out.dtype != torch.int32 or out.shape != (S, Hkv, L):
         raise ValueError("out must be int32 [S, Hkv, list_len]")
     if out_len is None:
-        out_len = torch.empty((S, Hkv), dtype=torch.int32, device=score.device)
+        out_len = _new(torch.empty, (S, Hkv), torch.int32, score.device, stream)
     elif out_len.dtype != torch.int32 or out_len.shape != (S, Hkv):
         raise ValueError("out_len must be int32 [S, Hkv]")
     dev = score.device
@@ -563,9 +582,10 @@ def fa_rows_validate(kv_rows: torch.Tensor, n_pool_rows: int, kv_len=None, strea
     a.kv_rows, a.list_len, a.S = _ptr(kv_rows), kv_rows.shape[1], kv_rows.shape[0]
     a.kv_len = _ptr(kv_len)
     a.n_pool_rows = int(n_pool_rows)
-    status = torch.empty(2, dtype=torch.int64, device=kv_rows.device)
-    _check(lib().fa_rows_validate(ctypes.byref(a), status.data_ptr(), _stream(stream, kv_rows.device)))
-    c, f = status.tolist()
+    with _made_for(stream, kv_rows.device):   # and read on
+        status = torch.empty(2, dtype=torch.int64, device=kv_rows.device)
+        _check(lib().fa_rows_validate(ctypes.byref(a), status.data_ptr(), _stream(stream, kv_rows.device)))
+        c, f = status.tolist()
     return int(c), int(f)
 
 
@@ -573,7 +593,7 @@ def fa_kv_page_table_to_rows(page_table: torch.Tensor, seq_len: torch.Tensor, li
                              out=None, stream=None) -> torch.Tensor:
     n_seq, max_pages = page_table.shape
     if out is None:
-        out = torch.empty((n_seq, list_len), dtype=torch.int32, device=page_table.device)
+        out = _new(torch.empty, (n_seq, list_len), torch.int32, page_table.device, stream)
     _check(lib().fa_kv_page_table_to_rows(_ptr(page_table), max_pages, _ptr(seq_len), n_seq, page_size, _ptr(out),
                                           list_len, _stream(stream, page_table.device)))
     return out
@@ -585,9 +605,9 @@ def fa_kv_quantize_int8(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_
     n, Hkv, D = x.shape
     R = n if n_pool_rows is None else int(n_pool_rows)
     if q is None:
-        q = torch.zeros((R, Hkv, D), dtype=torch.int8, device=x.device)
+        q = _new(torch.zeros, (R, Hkv, D), torch.int8, x.device, stream)
     if scale is None:
-        scale = torch.zeros((R // 64, Hkv, 64), dtype=torch.float16, device=x.device)
+        scale = _new(torch.zeros, (R // 64, Hkv, 64), torch.float16, x.device, stream)
     _check(lib().fa_kv_quantize_int8(_ptr(x), _DT[x.dtype], n, Hkv, D, _ptr(dst_rows), _ptr(q), _ptr(scale),
                                      q.shape[0], _stream(stream, x.device)))
     return q, scale
@@ -596,7 +616,7 @@ def fa_kv_quantize_int8(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_
 def fa_kv_dequantize_int8(q: torch.Tensor, scale: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     R, Hkv, D = q.shape
     if out is None:
-        out = torch.empty((R, Hkv, D), dtype=torch.float32, device=q.device)
+        out = _new(torch.empty, (R, Hkv, D), torch.float32, q.device, stream)
     _check(lib().fa_kv_dequantize_int8(_ptr(q), _ptr(scale), R, Hkv, D, _ptr(out), _stream(stream, q.device)))
     return out
 
@@ -607,9 +627,9 @@ def fa_kv_quantize_int4(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_
     n, Hkv, D = x.shape
     R = n if n_pool_rows is None else int(n_pool_rows)
     if q is None:
-        q = torch.zeros((R, Hkv, D // 2), dtype=torch.uint8, device=x.device)
+        q = _new(torch.zeros, (R, Hkv, D // 2), torch.uint8, x.device, stream)
     if scale is None:
-        scale = torch.zeros((R // 64, Hkv, 64), dtype=torch.float16, device=x.device)
+        scale = _new(torch.zeros, (R // 64, Hkv, 64), torch.float16, x.device, stream)
     _check(lib().fa_kv_quantize_int4(_ptr(x), _DT[x.dtype], n, Hkv, D, _ptr(dst_rows), _ptr(q), _ptr(scale),
                                      q.shape[0], _stream(stream, x.device)))
     return q, scale
@@ -618,7 +638,7 @@ def fa_kv_quantize_int4(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_
 def fa_kv_dequantize_int4(q: torch.Tensor, scale: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     R, Hkv, Dh = q.shape
     if out is None:
-        out = torch.empty((R, Hkv, 2 * Dh), dtype=torch.float32, device=q.device)
+        out = _new(torch.empty, (R, Hkv, 2 * Dh), torch.float32, q.device, stream)
     _check(lib().fa_kv_dequantize_int4(_ptr(q), _ptr(scale), R, Hkv, 2 * Dh, _ptr(out), _stream(stream, q.device)))
     return out
 
@@ -629,9 +649,9 @@ def fa_kv_quantize_fp8(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_r
     n, Hkv, D = x.shape
     R = n if n_pool_rows is None else int(n_pool_rows)
     if q is None:
-        q = torch.zeros((R, Hkv, D), dtype=torch.float8_e4m3fn, device=x.device)
+        q = _new(torch.zeros, (R, Hkv, D), torch.float8_e4m3fn, x.device, stream)
     if scale is None:
-        scale = torch.zeros((R // 64, Hkv, 64), dtype=torch.float16, device=x.device)
+        scale = _new(torch.zeros, (R // 64, Hkv, 64), torch.float16, x.device, stream)
     _check(lib().fa_kv_quantize_fp8(_ptr(x), _DT[x.dtype], n, Hkv, D, _ptr(dst_rows), _ptr(q), _ptr(scale),
                                     q.shape[0], _stream(stream, x.device)))
     return q, scale
@@ -640,7 +660,7 @@ def fa_kv_quantize_fp8(x: torch.Tensor, n_pool_rows: Optional[int] = None, dst_r
 def fa_kv_dequantize_fp8(q: torch.Tensor, scale: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     R, Hkv, D = q.shape
     if out is None:
-        out = torch.empty((R, Hkv, D), dtype=torch.float32, device=q.device)
+        out = _new(torch.empty, (R, Hkv, D), torch.float32, q.device, stream)
     _check(lib().fa_kv_dequantize_fp8(_ptr(q), _ptr(scale), R, Hkv, D, _ptr(out), _stream(stream, q.device)))
     return out
 
@@ -658,10 +678,10 @@ def fa_kv_sparse_rows(score: torch.Tensor, sinks: int, recent: int, k: int, list
     S, n_max = score.shape
     L = sinks + recent + k if list_len is None else int(list_len)
     if out is None:
-        out = torch.empty((S, L), dtype=torch.int32, device=score.device)
+        out = _new(torch.empty, (S, L), torch.int32, score.device, stream)
     if isinstance(workspace, str):
         nbytes = lib().fa_kv_sparse_rows_workspace_size(S, n_max)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=score.device)
+        workspace = _new(torch.empty, max(nbytes, 16), torch.uint8, score.device, stream)
     wptr = _ptr(workspace)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().fa_kv_sparse_rows(_ptr(score), n_max, _ptr(n_len), S, sinks, recent, k, _ptr(row_map), _ptr(out),
