@@ -239,6 +239,11 @@ fa_status fa_rows_prefill_heads(const fa_rows_args* a, void* ws, size_t ws_bytes
  * entry removes are zero, and so are those of a query whose lse is minus
  * infinity; positions at or past n_s keep their acc.  decay = 1 accumulates;
  * decay = 0 overwrites (acc is not read).  With S * Nq = 0 nothing is done.
+ * One list per slice (kv_rows [S, L]): lists per KV head have no such call.
+ * A term is as exact as lse, whose rounding (|lse| * 2^-24) is an error of the
+ * term's exponent: a dense mask that adds a number of large magnitude to every
+ * entry a query sees (-1e9 for a padded query, say) leaves no room in lse for
+ * the rest, so hide entries with minus infinity.
  *   acc      [S, Hkv, L] fp32
  *   pools    every kind of fa_rows_args, D <= 256 with 16-byte multiples per
  *            (row, KV head); any mask kind; any Nq and Hq / Hkv; L and Nq * Hq

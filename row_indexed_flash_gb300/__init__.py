@@ -324,7 +324,8 @@ def fa_rows_decode(q, k, v, kv_rows, scale, **kw):
 
     Keyword args: kv_len, mask (fp32 [S,Nq,L]), causal, k_scale/v_scale (int8
     pool, fp16 [R/64,Hkv,64]), out, lse, out_dtype, want_lse, n_valid_hint,
-    workspace (zero-initialised uint8 tensor), stream, check_status (read the
+    workspace (zero-initialised uint8 tensor), stream (what the call allocates
+    belongs to it; the current one if None), check_status (read the
     workspace status word after the call -- this synchronises -- and raise
     FA_ERR_WAIT_EXPIRED if a pipeline wait ran out, clearing the word).
     """

@@ -14,6 +14,11 @@
 // and one ordered pass writes the results after the CTAs have exchanged their
 // counts.  No scratch in global memory is needed.
 //
+// Keys beyond the first 40,960 of a CTA's positions do not fit beside and are
+// formed from global memory again in every pass: lists longer than 16 times that,
+// and, as the SMs are shared out, than twice that from 39 slices on and than
+// that from 77.
+//
 // Bound by latency: each of the five or six exchanges in a cluster costs about
 // as much as reading the CTA's totals.  Measured: two slices of 1,000 entries
 // 10 us, four of 99,936 entries and 8 KV heads (18 MB) 28 us.

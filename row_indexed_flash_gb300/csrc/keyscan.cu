@@ -35,9 +35,11 @@
 // four query vectors each (136 MB of keys and totals): 30 us, 4.6 TB/s; another
 // 16,384 rows per slice add 22 us, 6.3 TB/s (0.93 of the copy rate), so what
 // keeps the short call from it is about 6 us of start and end (a call of one
-// tile per CTA takes that).  INT8 33 us, INT4 32 us, E4M3 36 us: there the
-// widening holds it, not the bytes.  Scores of 32 sequences of 1k to 128k
-// tokens (58 MB of bounds) 21 us.
+// tile per CTA takes that).  INT8 33 us, INT4 32 us, E4M3 36 us: not the bytes
+// (INT4 has half of INT8's) nor widening as such (the quantised decode, where
+// some warps only copy and others only widen, takes in bytes at twice INT8's
+// rate here) but each key warp's own chain of copy, widen and wait for a stage.
+// Scores of 32 sequences of 1k to 128k tokens (58 MB of bounds) 22 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -1395,7 +1397,8 @@ __global__ void __launch_bounds__((kp::Shape<D, MODE>::THREADS), 1)
     // Two groups of four warps on alternate query tiles, each with a pair of
     // stages of its own (and an issuing warp that it alone feeds): the waits and
     // fences of one lie under the other's stores (16 x 128 queries, 1,562 blocks:
-    // 54 us, 58 with all eight warps at every tile).  At D 256 one group of
+    // 54 us, 58 with all eight warps at every tile; 55 since the keys are staged by
+    // warps).  At D 256 one group of
     // eight, as there is one pair.  Measured besides: the bounds in tensor
     // memory instead of shared memory, 55 us (a query tile 0.70 us for 0.76, but
     // a CTA starts 1 us later); all eight warps with two tiles of loads in

@@ -25,7 +25,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn() {
 }
 
 // The encodings of the last tensors, by everything an encoding depends on.  A
-// prefill call takes five maps and a decode call three, and every layer of a
+// prefill call takes five maps and a decode call two, and every layer of a
 // model has a pool of its own: sets of eight, found by a hash, hold those of 100
 // layers and more.  (The 32 that were searched in a row held six prefill layers.)
 struct TmapKey {
