@@ -123,14 +123,15 @@ typedef struct fa_rows_args {
  * Bytes of scratch (a device buffer, 256-byte aligned) that fa_rows_decode /
  * fa_rows_prefill need for these arguments; at least 256.  Layout: bytes
  * [0, 256) are the status block, whose first uint32 is the status word
- * (FA_WS_WAIT_EXPIRED; the next words are the calls' own scratch); decode
- * then holds one arrival counter per (slice, KV
- * head) and, when the list is split over several CTAs, the per-split partial
- * results.  The buffer must be ZERO-FILLED once after allocation
- * (fa_rows_workspace_init); every call leaves the counters at zero again, an
- * aborted one included.  One workspace must not be used by two calls that can
- * run at the same time.  Returns 0 and sets fa_last_error() on invalid
- * arguments.
+ * (FA_WS_WAIT_EXPIRED; the next words are the calls' own scratch); when decode
+ * splits the lists over several CTAs, one arrival counter per (slice, KV head)
+ * follows, and from byte 16384 on the per-split partial results (behind the
+ * counters where these need more).  The buffer must be ZERO-FILLED once after
+ * allocation (fa_rows_workspace_init); every call leaves the counters at zero
+ * again, an aborted one included, so calls of any arguments may use one
+ * workspace that is large enough for each in turn.  One workspace must not be
+ * used by two calls that can run at the same time.  Returns 0 and sets
+ * fa_last_error() on invalid arguments.
  */
 size_t fa_rows_workspace_size(const fa_rows_args* a, int is_prefill);
 fa_status fa_rows_workspace_init(void* ws, size_t ws_bytes, fa_stream_t stream);
@@ -182,7 +183,7 @@ fa_status fa_rows_decode(const fa_rows_args* a, void* ws, size_t ws_bytes, fa_st
  * device allocator or its callbacks, plugins whose framework owns every device
  * allocation, and latency-critical paths that cannot afford an allocation or
  * its failure.  Same arguments and results as fa_rows_decode, but the
- * split-merge scratch comes from a static device array of 16 MiB inside this
+ * split-merge scratch comes from a static device array (16 MiB and the counters) inside this
  * library (held on every GPU that loads it, until the process exits).
  * Arguments whose scratch would exceed 16 MiB are rejected with
  * FA_ERR_WORKSPACE before anything is launched.  The first call on a device

@@ -13,6 +13,7 @@
 #include "fa_internal.cuh"
 #include "kvread.cuh"
 #include "weights.cuh"
+#include "workspace.cuh"
 
 namespace {
 
@@ -112,6 +113,7 @@ struct DecodePlan {
   bool merge_kernel = false;   // the splits are merged by a kernel of their own
   size_t ws = 0;     // workspace bytes: status block, counters, partials
   size_t off_cnt = 0, off_ml = 0, off_o = 0;
+  size_t clear = 0;  // bytes of counters that the call itself zeroes
 };
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -255,11 +257,17 @@ fa_status plan_decode(const fa_rows_args* a, DecodePlan* pl) {
   // splits: 4.9 us of in-kernel merge).
   pl->merge_kernel = pl->tc && !pl->tcq && pl->nsplit > 1 && units * pl->nsplit <= slots &&
                      pl->chunk <= 4 * align;
-  // [status block][counters][(max, sum) partials][O partials]
+  // [status block][counters][(max, sum) partials][O partials]; see workspace.cuh
   const size_t nunit = (size_t)units;
   const size_t cnt_bytes = round_up(nunit * sizeof(unsigned int), 256);
-  pl->ws = pl->off_cnt + cnt_bytes;
+  pl->ws = pl->off_cnt;
   if (pl->nsplit > 1) {
+    pl->ws = far::kFixedBytes;
+    if (nunit > far::kFixedUnits) {
+      pl->off_cnt = far::kFixedBytes;
+      pl->ws += cnt_bytes;
+      pl->clear = pl->merge_kernel ? 0 : cnt_bytes;
+    }
     const size_t ml_bytes = round_up(nunit * pl->nsplit * pl->rows * 2 * sizeof(float), 256);
     const size_t o_bytes = nunit * pl->nsplit * pl->rows * (size_t)a->D * sizeof(float);
     pl->off_ml = pl->ws;
@@ -362,7 +370,7 @@ static fa_status decode_call(const fa_rows_args* a, bool head_lists, void* ws, s
   p.lse = a->lse;
   {
     char* w = static_cast<char*>(ws);
-    p.counters = reinterpret_cast<unsigned int*>(w + pl.off_cnt);
+    p.counters = reinterpret_cast<unsigned int*>(w + pl.off_cnt);   // read where there are splits
     if (pl.nsplit > 1) {
       p.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
       p.part_o = reinterpret_cast<float*>(w + pl.off_o);
@@ -386,6 +394,10 @@ static fa_status decode_call(const fa_rows_args* a, bool head_lists, void* ws, s
   p.merge_kernel = pl.merge_kernel ? 1 : 0;
   p.head_lists = head_lists ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (pl.clear) {
+    const cudaError_t z = cudaMemsetAsync(p.counters, 0, pl.clear, s);
+    if (z != cudaSuccess) return cuda_fail(z, "counter clear");
+  }
   cudaError_t e = cudaErrorInvalidValue;
   const int kind = kv_kind(a->kv_dtype);
   if (pl.tc) {

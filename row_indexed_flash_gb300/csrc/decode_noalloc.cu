@@ -20,6 +20,7 @@
 #include <atomic>
 
 #include "fa_internal.cuh"
+#include "workspace.cuh"
 
 namespace far {
 void set_last_error(const char* msg);  // the message fa_last_error() returns
@@ -27,9 +28,10 @@ void set_last_error(const char* msg);  // the message fa_last_error() returns
 
 namespace {
 
-constexpr size_t kStaticScratchBytes = 16u << 20;  // 16 MiB
+constexpr size_t kStaticScratchBytes = 16u << 20;  // 16 MiB, beside the status block and counters
+constexpr size_t kStaticArrayBytes = kStaticScratchBytes + far::kFixedBytes;
 
-static __device__ __align__(256) unsigned char g_decode_scratch[kStaticScratchBytes];
+static __device__ __align__(256) unsigned char g_decode_scratch[kStaticArrayBytes];
 
 // Device address of the scratch array for the current device, looked up once
 // per device.  In host code the array's name is only a host-side stand-in, so
@@ -64,7 +66,7 @@ fa_status fa_rows_decode_static(const fa_rows_args* a, fa_stream_t stream) {
   if (!a) return fa_rows_decode(a, nullptr, 0, stream);  // reports the NULL argument
   const size_t need = fa_rows_workspace_size(a, 0);
   if (need == 0 && fa_last_error()[0] != 0) return fa_rows_decode(a, nullptr, 0, stream);  // invalid arguments
-  if (need > kStaticScratchBytes) {
+  if (need > kStaticArrayBytes) {
     char msg[256];
     snprintf(msg, sizeof(msg),
              "fa_rows_decode_static: these arguments need %zu bytes of scratch; the static array holds %zu", need,
@@ -85,7 +87,7 @@ fa_status fa_rows_decode_static(const fa_rows_args* a, fa_stream_t stream) {
     const fa_status st = fa_rows_workspace_init(ws, need, stream);
     if (st != FA_OK) return st;
   }
-  return fa_rows_decode(a, ws, kStaticScratchBytes, stream);
+  return fa_rows_decode(a, ws, kStaticArrayBytes, stream);
 }
 
 }  // extern "C"
