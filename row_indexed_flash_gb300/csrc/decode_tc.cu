@@ -32,9 +32,9 @@
 //                  end the split's (max, sum, O) or the final output.
 // INT8 pools (codes with one fp16 scale per (row, KV head)) take the same
 // pipeline with all four producer warps on both matrices: they gather the
-// codes into the upper half of the stage's tiles, widen them in place to Q's
-// 16-bit type (exact: |code| <= 127), and store the rows' scales beside the
-// tile; the softmax folds the K scale into the logit and the V scale into P,
+// codes into the upper half of the stage's tiles, widen them in place, K to Q's
+// 16-bit type and V to bf16 (exact: |code| <= 127), and store the rows' scales
+// beside the tile; the softmax folds the K scale into the logit and the V scale into P,
 // so the MMAs see plain 16-bit operands.
 // The last CTA to finish a (slice, KV head) merges the splits (an arrival
 // counter in the workspace, reset by that CTA; nothing waits on it).
@@ -136,7 +136,7 @@ __device__ __forceinline__ void dk_softmax(const DecodeParams& p, unsigned char*
   const unsigned long long wait_ns = p.wait_ns;
   const int lane = threadIdx.x & 31;
   const int G = p.G, QV = p.QV;
-  const bool bf16 = p.q_bf16 != 0;
+  const bool bf16 = KQ != 0 || p.q_bf16 != 0;   // P's type
     // Only rows 0..QV-1 of S are real.  After the tensor-memory load (one row
     // per lane), the real rows are spread over all 32 lanes through shared
     // memory: LPR = 32/QVP lanes per row, CPL = BN/LPR columns per lane, so
@@ -152,9 +152,9 @@ __device__ __forceinline__ void dk_softmax(const DecodeParams& p, unsigned char*
     const float c = p.qscale;
     const uint32_t tO = tbase + Sh::COL_O;
     float m_used = NEG_INF, l = 0.f;            // state of row `row`, held by its LPR lanes
-    // INT8 with f16 queries: P * s_v reaches 256 * 65504 / 127, beyond f16, so
-    // it is carried as P * s_v * 2^-8 and O multiplied back by 2^8 at the end
-    const float pv_scale = (KQ != 0 && !bf16) ? 0.00390625f : 1.f;
+    // INT8: P * s_v lies anywhere between 2^-24 and 2^24, beyond f16 at either
+    // end, so P and the V tile are bf16 whatever the queries are (with f16
+    // P * s_v * 2^-8, terms below 2^-14 lost their bits: outputs 5e-3 off)
     bool ok = true;
     // List entries lane and lane + 32 of tile j (cur) and j + 1 (nx), loaded
     // ahead so no wait lands on their latency; INT8 scales of those entries
@@ -271,10 +271,10 @@ __device__ __forceinline__ void dk_softmax(const DecodeParams& p, unsigned char*
         const float p0 = fast_ex2(x[2 * kk] - mu), p1 = fast_ex2(x[2 * kk + 1] - mu);
         sum += p0 + p1;
         float a0 = p0, a1 = p1;
-        if constexpr (KQ != 0) {   // the V scale of each column rides on P (times 2^-8 in f16)
+        if constexpr (KQ != 0) {   // the V scale of each column rides on P
           const float2 sv = *reinterpret_cast<const float2*>(scK + BN + 2 * pp);
-          a0 *= sv.x * pv_scale;
-          a1 *= sv.y * pv_scale;
+          a0 *= sv.x;
+          a1 *= sv.y;
         }
         const uint32_t hi = pack2h(a0, a1, bf16);
         float h0, h1;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void dk_softmax(const DecodeParams& p, unsigned char*
       const int i = r / G, h = g * G + r % G;
       const size_t oi = ((size_t)s * p.Nq + i) * p.Hq + h;
       const size_t pi = (unit * p.nsplit + split) * QV + r;
-      const float inv = l_r > 0.f ? 1.f / l_r / pv_scale : 0.f;
+      const float inv = l_r > 0.f ? 1.f / l_r : 0.f;
 #pragma unroll
       for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t o[32];
@@ -360,11 +360,10 @@ __device__ __forceinline__ void dk_softmax(const DecodeParams& p, unsigned char*
           for (int k = 0; k < 32; ++k) store_out(p.out, oi * D + c4 * 32 + k, __uint_as_float(o[k]) * inv, p.out_dtype);
         } else if (m_r != NEG_INF) {
           float4* dst = reinterpret_cast<float4*>(p.part_o + pi * D + c4 * 32);
-          const float os = 1.f / pv_scale;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]) * os, __uint_as_float(o[4 * k + 1]) * os,
-                                 __uint_as_float(o[4 * k + 2]) * os, __uint_as_float(o[4 * k + 3]) * os);
+            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                 __uint_as_float(o[4 * k + 3]));
         }
       }
       if (own) {
@@ -575,8 +574,9 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
             const int f = it * 32 + lane;
             const int e = pw * ROWS + f / Sh::CPRQ, c = f % Sh::CPRQ;
             // 16 codes = columns 16c .. 16c+15: two 16-byte chunks of atom c / 4
-            const uint2 a = widen_i8x4(cw[it].x, bf16), b = widen_i8x4(cw[it].y, bf16);
-            const uint2 cc = widen_i8x4(cw[it].z, bf16), d = widen_i8x4(cw[it].w, bf16);
+            const bool to_bf16 = mat || bf16;   // K in the queries' type, V in P's
+            const uint2 a = widen_i8x4(cw[it].x, to_bf16), b = widen_i8x4(cw[it].y, to_bf16);
+            const uint2 cc = widen_i8x4(cw[it].z, to_bf16), d = widen_i8x4(cw[it].w, to_bf16);
             unsigned char* row = tile + (c / 4) * Sh::KV_ATOM + e * 128;
             const int k0 = 2 * (c % 4);
             *reinterpret_cast<uint4*>(row + ((k0 ^ (e & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(dk::NWARP * 32, 2)
       // about two thirds of the M=128 time at N=64; PV stays at M=128, where
       // M=64 takes as long.
       const uint32_t id_qk = make_idesc_f16(QVP <= 16 ? 64 : 128, BN, bf16, false);
-      const uint32_t id_pv = make_idesc_f16(128, D, bf16, true);
+      const uint32_t id_pv = make_idesc_f16(128, D, KQ != 0 || bf16, true);
       // operand descriptors built once; each MMA adds a constant offset
       const uint64_t dQ = sdesc_sw128(smem_u32(sm + Sh::OFF_Q), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sm + Sh::OFF_K), 16, 1024);

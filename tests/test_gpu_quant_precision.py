@@ -53,3 +53,37 @@ def test_outputs_of_values_that_cancel(kv, S, Nq, Hq, Hkv, L, heads):
             size = np.repeat(np.abs(v).mean(axis=0), Hq // Hkv, axis=0)
             err = np.abs(out[i] - want[None]) / size[None]
             assert err.max() <= 2.0 ** -12 + 2.0 ** -14, (i, err.max())
+
+
+@pytest.mark.parametrize("heads", [False, True])
+@pytest.mark.parametrize("qtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,S,Nq,Hq,Hkv,L", [(256, 1, 1, 2, 2, 3008), (256, 2, 1, 8, 2, 700), (256, 40, 2, 8, 8, 1000),
+                                          (256, 1, 1, 8, 1, 64), (128, 2, 1, 8, 2, 3008), (64, 2, 1, 8, 2, 3008)])
+@pytest.mark.parametrize("depth", [2.0, 5.0, 9.0])
+def test_int8_outputs_of_small_weights(depth, D, S, Nq, Hq, Hkv, L, qtype, heads):
+    """One entry with logit 0, the others with -depth, and every value v = 1 code times its scale: the output is v
+    times the sum of the rounded P over the sum of P.
+
+    P is carried to 16 bits (2^-17) or is one f16 weight of its own reference (2^-12, the quantised kernel at D 128);
+    the tensor core's sums take at most 8 steps per tile of 64 keys, 376 in all, each cut off by at most 2^-23, and
+    the row sums some 2^-23: 2^-14 and 2^-11.5 bound them.
+    """
+    R = 4096
+    g = synth.rng(930)
+    rows = np.stack([g.permutation(R)[:L] for _ in range(S)]).astype(np.int32)
+    rows[:, 0] = 0
+    rows[:, 1:][rows[:, 1:] == 0] = 1
+    k = torch.zeros((R, Hkv, D), dtype=torch.int8, device="cuda")
+    k[1:, :, 0] = -1
+    v = torch.ones((R, Hkv, D), dtype=torch.int8, device="cuda")
+    ones = torch.ones((R // 64, Hkv, 64), dtype=torch.float16, device="cuda")
+    q = torch.zeros((S, Nq, Hq, D), dtype=qtype, device="cuda")
+    q[..., 0] = 1.0
+    rd, fn = torch.from_numpy(rows).cuda(), far.fa_rows_decode
+    if heads:
+        rd, fn = rd[:, None].repeat(1, Hkv, 1), far.fa_rows_decode_heads
+    for scale in (0.0241, 0.9, 500.0):
+        vs = ones * scale
+        out, _ = fn(q, k, v, rd, depth, k_scale=ones, v_scale=vs, check_status=True)
+        err = (out.double() / vs[0, 0, 0].double() - 1).abs().max().item()
+        assert err <= (2.0 ** -11.5 if D == 128 else 2.0 ** -14), (scale, err)
