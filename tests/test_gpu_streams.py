@@ -64,7 +64,7 @@ def test_outputs_do_not_take_memory_that_the_current_stream_still_reads():
     table = torch.arange(64, dtype=torch.int32, device="cuda")[None].repeat(2, 1)
     lens = torch.full((2,), 4096, dtype=torch.int32, device="cuda")
     lo, hi = (torch.zeros((64, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    score = torch.rand((2, 2, 64), device="cuda")
+    score, first = torch.rand((2, 2, 64), device="cuda"), acc[:, 0].contiguous()
     head_rows = rows[:, None].repeat(1, 2, 1)
     x = dev_bits(synth.normal_bits(synth.rng(701), (4096, 2, 128), "bf16"), "bf16")
     other = torch.cuda.Stream()
@@ -77,7 +77,7 @@ def test_outputs_do_not_take_memory_that_the_current_stream_still_reads():
         lambda s: far.fa_kv_block_rows(score, table, lens, 1, 1, 6, stream=s),
         lambda s: (far.fa_kv_page_table_to_rows(table, lens, 4096, stream=s),),
         lambda s: far.fa_kv_quantize_int8(x, 4096, stream=s),
-        lambda s: (far.fa_kv_sparse_rows(acc[:, 0].contiguous(), 4, 8, 100, stream=s),),
+        lambda s: (far.fa_kv_sparse_rows(first, 4, 8, 100, stream=s),),
     ]
     for i, call in enumerate(calls):
         outs = call(None)                              # warm, and the sizes of what the call allocates
