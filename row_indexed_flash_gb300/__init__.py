@@ -196,26 +196,42 @@ def _new(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
+def _capturing(stream, device) -> bool:
+    with _made_for(stream, device):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _captured_ws(nbytes: int, device, stream_handle: int, stream, counters: bool = False) -> torch.Tensor:
+    """Scratch of one call that is being captured: of the graph alone, so that graphs may be replayed in any
+    order and side by side.  Split counters (counters) are zeroed by the graph itself; nothing else of it has to
+    be, as no one can read its status word."""
+    buf = _new(torch.empty, max(nbytes, 256), torch.uint8, device, stream)
+    if counters:
+        _check(lib().fa_rows_workspace_init(buf.data_ptr(), min(buf.numel(), 16384), stream_handle))
+    return buf
+
+
 class _Workspace:
     """Caller-side scratch (status word, split counters, partials): grown on demand, zeroed once."""
 
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
 
-    def get(self, nbytes: int, device, stream_handle: int, stream=None) -> Tuple[int, int]:
-        if nbytes == 0:
-            return 0, 0
+    def get(self, nbytes: int, device, stream_handle: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
+            if _capturing(stream, device):
+                return _captured_ws(nbytes, device, stream_handle, stream)
             self.buf = _new(torch.empty, max(nbytes, 1 << 20), torch.uint8, device, stream)
             _check(lib().fa_rows_workspace_init(self.buf.data_ptr(), self.buf.numel(), stream_handle))
-        return self.buf.data_ptr(), self.buf.numel()
+        return self.buf
 
 
 _workspaces = {}
 
 
 def _default_ws(device, stream_handle, is_prefill: bool) -> _Workspace:
-    """The binding's own workspace for calls without one: one per (device, stream, decode or prefill)."""
+    """The binding's own workspace for calls without one: one per (device, stream, decode or prefill).
+    A call that is captured into a graph has one to itself instead."""
     key = (device, stream_handle, bool(is_prefill))
     if key not in _workspaces:
         _workspaces[key] = _Workspace()
@@ -305,14 +321,18 @@ def _attend(entry: str, is_prefill: bool, q, k, v, kv_rows, scale, *, workspace=
     sh = _stream(stream, q.device)
     need = fa_rows_workspace_size(a, is_prefill)
     if workspace is None:
-        wsobj = _default_ws(q.device, sh, is_prefill)
-        wptr, wbytes = wsobj.get(need, q.device, sh, stream)
-        wtensor = wsobj.buf
+        if _capturing(stream, q.device):
+            # one launch with partials: the splits are counted and merged in it
+            counters = need > 256 and not is_prefill and lib().fa_rows_decode_launches(ctypes.byref(a)) == 1
+            wtensor = _captured_ws(need, q.device, sh, stream, counters)
+        else:
+            wtensor = _default_ws(q.device, sh, is_prefill).get(need, q.device, sh, stream)
+        wptr, wbytes = wtensor.data_ptr(), wtensor.numel()
     else:
         wptr, wbytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         wtensor = workspace
     _check(getattr(lib(), entry)(ctypes.byref(a), wptr, wbytes, sh))
-    if check_status and wtensor is not None:
+    if check_status:
         word = fa_rows_status(wtensor, clear=True, stream=stream)
         if word & FA_WS_WAIT_EXPIRED:
             raise FaRowsError(FA_ERR_WAIT_EXPIRED, f"{entry}: a pipeline wait ran out; the outputs are invalid")
@@ -366,9 +386,8 @@ def _status_ws(workspace, device, sh, stream, need: int = 256):
     need the status block alone."""
     if workspace is not None:
         return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
-    wsobj = _default_ws(device, sh, True)
-    wptr, wbytes = wsobj.get(need, device, sh, stream)
-    return wptr, wbytes, wsobj.buf
+    buf = _default_ws(device, sh, True).get(need, device, sh, stream)
+    return buf.data_ptr(), buf.numel(), buf
 
 
 def _raise_expired(entry: str, wtensor, stream):
