@@ -83,6 +83,12 @@ struct TreeShape {
   static constexpr int CODES = BN * ROW;             // code bytes of a tile and matrix
   static constexpr int NC = QUANT ? 49152 / (2 * CODES) : 0;   // code stages
   static constexpr int NSC = QUANT ? 8 : 0;                    // stages of scales
+  // Slots for the notes of values that are not finite, a unit each in turn.  The end of unit u clears the slot that
+  // unit u - 1 has read and unit u + NODD - 1 is to write.  Softmax warps, which write the notes of 16-bit pools, are at unit
+  // u + 1 at most by then.  Wideners, which write those of codes, run ahead by the V stages: one at a unit w has the PV of
+  // NSTV tiles before behind it, which is of unit w - NSTV or a later one (a unit has a tile at least), and the first
+  // product of that into O waited for the end of the unit before.  So unit w's slot is clear by the end of w - NSTV - 1.
+  static constexpr int NODD = QUANT ? NSTV + 2 : 3;
   static constexpr int NSMX = 4 * NG;                  // softmax warps
   static constexpr int W_LOAD = NSMX, W_MMA = NSMX + LOADERS, W_WIDE = W_MMA + NG;
   static constexpr int NWARP = W_WIDE + (QUANT ? kTtWideners : 0);
@@ -98,8 +104,8 @@ struct TreeShape {
   // comb [4], c_full, c_empty [NC]
   static constexpr int NBAR = 5 + 2 * NSTK + 2 * NSTV + 12 + 4 + 2 * NC;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;                // tensor memory's address, abort flag
-  static constexpr int OFF_ODD = OFF_MISC + 16;                      // [3][kTtWords] nodes with a V not finite, a unit in turn
-  static constexpr int OFF_GATH = OFF_ODD + 3 * kTtWords * 4;         // [16] a stage was gathered: K, V
+  static constexpr int OFF_ODD = OFF_MISC + 16;                      // [NODD][kTtWords] nodes with a V not finite
+  static constexpr int OFF_GATH = OFF_ODD + NODD * kTtWords * 4;      // [16] a stage was gathered: K, V
   static constexpr int OFF_IDX = OFF_GATH + 16 * 4;         // [loaders][64] rows of the tile a loader is on
   static constexpr int OFF_KIN = OFF_IDX + LOADERS * BN * 4;    // [NG][128][kTtWords] lines
   static constexpr int OFF_X = OFF_KIN + NG * kTtM * kTtWords * 4;   // [2 unit parities][2 groups][reference, sum][128]
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       }
     }
     *abort_flag = 0;
-    for (int i = 0; i < 3 * kTtWords; ++i) odd[i] = 0u;
+    for (int i = 0; i < C::NODD * kTtWords; ++i) odd[i] = 0u;
     mbar_fence_init();
   }
   if (warp == C::W_MMA) {
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
         const int t_lo = x - u.first, t_hi = min(u.tiles, hi - u.first);
         int base = 0;
         if constexpr (KIND == KV_F8) base = tree_len(p, u.s) - tree_nodes(p, u.s);
-        uint32_t* odd_u = odd + ui % 3 * kTtWords;
+        uint32_t* odd_u = odd + ui % C::NODD * kTtWords;
         for (int t = t_lo; t < t_hi; ++t, ++jj) {
           const int sc = jj % NC, sk = jj % NSTK, sv = jj % NSTV;
           unsigned char* codes = sm + C::OFF_C + sc * 2 * C::CODES;
@@ -700,7 +706,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       const bool idle = !QUANT && !__any_sync(0xffffffffu, live);
       const int32_t* rows_u = p.kv_rows + (size_t)u.s * p.L;
       const int step = alt ? 2 : 1, start = alt ? (grp - jj0) & 1 : 0;
-      uint32_t* odd_u = odd + ui % 3 * kTtWords;
+      uint32_t* odd_u = odd + ui % C::NODD * kTtWords;
       // list entries of the group's next tile, loaded a tile ahead
       int nxt[2];
 #pragma unroll
@@ -879,8 +885,8 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // This wait says that the unit before is behind every warp (its sums were read before this one's first
-      // product into O went out): its notes make room for the unit after the next.
-      if (threadIdx.x < kTtWords) odd[(ui + 2) % 3 * kTtWords + threadIdx.x] = 0u;
+      // product into O went out): its notes make room for those of unit ui + NODD - 1, whose writers wait for this end.
+      if (threadIdx.x < kTtWords) odd[(ui + C::NODD - 1) % C::NODD * kTtWords + threadIdx.x] = 0u;
       tc_fence_after();
       // this thread's columns: with alternate tiles half of both groups' sums, joined at the larger
       // reference; else all of its own
