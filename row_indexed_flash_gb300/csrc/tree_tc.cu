@@ -37,7 +37,8 @@
 //
 // Entries hidden by the tree have weight 0, but 0 * V is NaN where V is not finite.  Such values of nodes are
 // therefore taken out of the staged V (by the softmax warps, of E4M3 codes by the wideners), and the rows that do see their
-// node get them back at the end.
+// node get them back at the end.  An infinity in the context of a 16-bit pool has a weight above 0, but the low part of that
+// weight may be 0 or negative and a small one rounds to 0: a sum that came out NaN is looked up again at a unit's end.
 //
 // Every wait is bounded in time, as in the other tensor-core kernels.
 #include <cuda.h>
@@ -180,6 +181,27 @@ __device__ __forceinline__ uint4 codes_i4x8(uint32_t w) {
   constexpr uint32_t k43 = 0x43434343u, k136 = 0x43084308u;
   return make_uint4(sub_bf16x2(__byte_perm(p, k43, 0x4140u), k136), sub_bf16x2(__byte_perm(p, k43, 0x4342u), k136),
                     sub_bf16x2(__byte_perm(q, k43, 0x4140u), k136), sub_bf16x2(__byte_perm(q, k43, 0x4342u), k136));
+}
+// Infinities among V's columns col .. col + 15 of KV head g, list positions lo .. hi - 1 of `rows`: bit k a +inf in column
+// col + k, bit 16 + k a -inf, both bits for a NaN.  A whole warp calls it.
+template <bool BF16>
+__device__ __forceinline__ uint32_t odd_columns(const TreeParams& p, const int32_t* rows, int lo, int hi, int g, int col) {
+  constexpr uint32_t INF = BF16 ? 0x7f80u : 0x7c00u;
+  uint32_t found = 0;
+#pragma unroll 1
+  for (int pos = lo + (int)(threadIdx.x & 31); pos < hi; pos += 32) {
+    const int row = __ldg(rows + pos);
+    if (row < 0 || (long long)row >= p.R) continue;
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + ((size_t)row * p.Hkv + g) * p.D + col);
+    const uint4 a = __ldg(at), b = __ldg(at + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t h = (w[k >> 1] >> (16 * (k & 1))) & 0xffffu, mag = h & 0x7fffu;
+      if (mag >= INF) found |= mag > INF ? 0x10001u << k : h >> 15 ? 0x10000u << k : 1u << k;
+    }
+  }
+  return __reduce_or_sync(0xffffffffu, found);
 }
 // 32 logits of a chunk: y = S * scale (quantised pools), hidden ones -inf.
 __device__ __forceinline__ void scale32(uint32_t (&sv)[32], const float* ksc) {
@@ -936,6 +958,22 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
           tmem_ld16(tO + col, r);
 #pragma unroll
           for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(r[k]);
+        }
+        if constexpr (!QUANT) {
+          // a sum that is NaN though the weights are not: infinities of the context, which every node sees
+          bool nan = false;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) nan = nan || y[k] != y[k];
+          nan = nan && live && lt == lt;
+          if (__any_sync(0xffffffffu, nan)) {
+            const uint32_t found = odd_columns<PAIR>(p, rows_u, t_lo * BN, min(min(t_hi * BN, n_s), base), u.g, col);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t signs = (found >> k) & 0x10001u;
+              if (nan && y[k] != y[k] && (signs == 1u || signs == 0x10000u))
+                y[k] = __uint_as_float(signs == 1u ? 0x7f800000u : 0xff800000u);
+            }
+          }
         }
         if (!row_ok) continue;
         if (any_odd) {

@@ -41,3 +41,31 @@ def test_a_nan_in_one_nodes_v_reaches_exactly_those_that_see_it(kv, q, S, T, Hq,
         out, lse = p.call(check_status=True)
         assert torch.equal(lse, want_lse)
         assert same_but_nan(out, want)
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 64), ("f16", 128), ("f16", 256)])
+@pytest.mark.parametrize("T,Hq,L,spread", [(5, 8, 150, 1.0), (40, 32, 700, 1.0), (12, 8, 9000, 1.0), (5, 8, 190, 12.0)])
+def test_infinities_of_the_context_come_out_as_infinities(kv, D, T, Hq, L, spread):
+    """Every node sees them with a weight above 0: an infinity where all of a component have one sign, else NaN.  spread: the
+    weights go down to e^-80 of the largest, far below the 16-bit types of the product."""
+    p = Problem(60, kv=kv, q=kv, S=2, T=T, Hq=Hq, Hkv=2, D=D, L=L, layout="pages", nodes=[T, T - 2], amp=spread,
+                scale=0.3 * D ** -0.5 * 3)
+    want, want_lse = p.call()
+    G, inf, nan = Hq // 2, float("inf"), float("nan")
+    for s, live in ((0, T), (1, T - 2)):
+        for entries, h, c, x, to in (([0], 0, 5, [inf], inf), ([L // 2], 1, 7, [-inf], -inf), ([3, 70], 0, D - 1, [inf, -inf], nan),
+                                     ([L - T - 1], 1, 16, [nan], nan), ([9, 80, 90], 1, 17, [-inf] * 3, -inf)):
+            for e, y in zip(entries, x):
+                p.v[int(p.rows[s, e]), h, c] = y
+            want[s, :live, h * G:(h + 1) * G, c] = to
+    out, lse = p.call()
+    assert torch.equal(lse, want_lse) and same_but_nan(out, want)
+
+
+def test_every_value_of_a_long_context_infinite():
+    p = Problem(61, S=1, T=4, L=100000, layout="pages", Hq=2, Hkv=1)
+    p.v[:, 0, ::2] = float("inf")
+    p.v[:, 0, 1::2] = float("-inf")
+    p.v[p.rows[0, -4:].long()] = 1.0                       # the nodes' own are finite
+    out, _ = p.call(check_status=True)
+    assert (out[..., ::2] == float("inf")).all() and (out[..., 1::2] == float("-inf")).all()
