@@ -20,12 +20,14 @@
 // Measured on 16 sequences of 2k to 32k tokens in pages, 32/8 heads, 64 nodes (bf16, 768 MB): tiles of 128, one S a group
 // and one issuer of one lane 313 us; tiles of 64 with two S 398, the issuer busy throughout; two issuers 324; converged
 // warps 259; barriers that a poll has seen not waited for again, and asked side by side, 254; warps without a node idle,
-// 249 (3.1 TB/s); one product for both S of a group 293, since it waits for both.  An f16 pool 218.  INT8 codes, 24 nodes
+// 249 (3.1 TB/s); one product for both S of a group 293, since it waits for both.  An f16 pool 256.  INT8 codes, 24 nodes
 // (389 MB): 167.  4 x 16,384 shuffled bf16 rows, 16 nodes (270 MB): 76 (3.6 TB/s).
 //
 // The softmax keeps a reference per row that moves only when the maximum has grown by
-// more than 2^8 (then O is rescaled in tensor memory); P goes over S as f16 (11 bits) for f16 pools and as the pair rn(P),
-// rn(P - rn(P)) for bf16 ones (a bf16 V needs bf16 weights, and 8 bits of them would move outputs by 2^-9).
+// more than 2^8 (then O is rescaled in tensor memory); over 16-bit pools P goes over S as the pair rn(P), rn(P - rn(P)) of
+// V's type, as in the decode kernel: one bf16 value (8 bits) would move outputs by up to 2^-9, one f16 value (11 bits) by up to
+// 2^-12, and a token would be scored less exactly in a tree than decoded (f16 pool, 64 nodes: 217 us with one value, 256
+// with the pair).
 //
 // Quantised pools (INT8, INT4, FP8 E4M3 codes with an fp16 scale per row and KV head; D 128):
 //   codes      arrive in a ring of their own, their scales beside them
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
     tree_tc_kernel(const __grid_constant__ TreeTcParams kp, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = TreeShape<D, KIND>;
-  constexpr bool QUANT = C::QUANT, PAIR = KIND == KV_BF16;
+  constexpr bool QUANT = C::QUANT, PAIR = !QUANT, PBF16 = KIND == KV_BF16;   // P: two values, of bf16
   constexpr int BN = C::BN, NG = C::NG, LOADERS = C::LOADERS, NB = C::NB, NSTK = C::NSTK, NSTV = C::NSTV, NC = C::NC;
   const TreeParams& p = kp.a;
   const unsigned long long wait_ns = p.wait_ns;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       // free (its PV has been issued) and the K stage is there, a PV once its P is written and its V stage there.
       const int g = warp - C::W_MMA;
       const uint32_t id_qk = make_idesc_f16(kTtM, BN, QBF16, false);
-      const uint32_t id_pv = make_idesc_f16(kTtM, D, PAIR, true);
+      const uint32_t id_pv = make_idesc_f16(kTtM, D, PBF16, true);
       const uint64_t dQ = sdesc_at(sdesc_sw128(smem_u32(sm + C::OFF_Q), 16, 1024), alt ? 0 : g * C::QTILE);
       const uint64_t dK = sdesc_sw128(smem_u32(sm + C::OFF_K), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(sm + C::OFF_V), C::BLK, 1024);
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       // weights are exp2(logit - ref), sums relative to it.  shift: how far the reference stands above the largest
       // logit when it is set (-7 for f16 weights; above V scales for quantised pools)
       float ref = NEG_INF, l = 0.f;
-      float shift = PAIR ? 0.f : QUANT ? -14.f - kTtLift : -kTtLift;
+      float shift = PBF16 ? 0.f : QUANT ? -14.f - kTtLift : -kTtLift;
       for (int j = start; j < n; j += step, ++done) {
         const int jb = (t_lo + j) * BN;   // list position of the tile's first entry
         uint32_t bits[2];
@@ -838,12 +840,13 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
                     pr.y = (bits[q] >> (i + 1)) & 1u ? pr.y : 0.f;
                   }
                 }
-                const uint32_t h = pack2h(pr.x, pr.y, PAIR);
+                const uint32_t h = pack2h(pr.x, pr.y, PBF16);
                 w[k] = h;
                 if constexpr (PAIR) {
-                  const float2 rem =
-                      __fadd2_rn(pr, make_float2(-__uint_as_float(h << 16), -__uint_as_float(h & 0xffff0000u)));
-                  w[4 + k] = pack2h(rem.x, rem.y, true);
+                  const float2 hi =
+                      PBF16 ? make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)) : f16x2_to_f2(h);
+                  const float2 rem = __fadd2_rn(pr, make_float2(-hi.x, -hi.y));
+                  w[4 + k] = pack2h(rem.x, rem.y, PBF16);
                 }
               }
               const uint32_t col = tS + (2 * q + (o >> 1)) * 16 + (o & 1) * 4;
@@ -859,7 +862,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
           const int st = (jj0 + j) % NSTV;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_full + st, ((jj0 + j) / NSTV) & 1, abort_flag, wait_ns)))) break;
           unsigned char* vt = sm + C::OFF_V + st * C::TILE;
-          constexpr uint32_t ADD = PAIR ? 0x00800080u : 0x04000400u;   // carries a magnitude that is not finite into bit 15
+          constexpr uint32_t ADD = PBF16 ? 0x00800080u : 0x04000400u;   // carries a magnitude that is not finite into bit 15
           for (int f = m; f < C::TILE / 16; f += 128) {
             uint4* at = reinterpret_cast<uint4*>(vt) + f;
             const int k = jb + (f * 16 % C::BLK) / 128 - base;
@@ -966,7 +969,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
           for (int k = 0; k < 16; ++k) nan = nan || y[k] != y[k];
           nan = nan && live && lt == lt;
           if (__any_sync(0xffffffffu, nan)) {
-            const uint32_t found = odd_columns<PAIR>(p, rows_u, t_lo * BN, min(min(t_hi * BN, n_s), base), u.g, col);
+            const uint32_t found = odd_columns<PBF16>(p, rows_u, t_lo * BN, min(min(t_hi * BN, n_s), base), u.g, col);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const uint32_t signs = (found >> k) & 0x10001u;
@@ -991,7 +994,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
                     y[t] = __int_as_float(0x7fc00000);
                 } else {
                   const uint32_t h = __ldg(static_cast<const uint16_t*>(p.v) + at + t);
-                  const float f = PAIR ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+                  const float f = PBF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
                   if (!isfinite(f)) y[t] += f;
                 }
               }

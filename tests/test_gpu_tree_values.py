@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import synth
-from branch_helpers import kin_of
+from branch_helpers import assert_near, kin_of
 from test_gpu_tree import Problem
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +69,12 @@ def test_every_value_of_a_long_context_infinite():
     p.v[p.rows[0, -4:].long()] = 1.0                       # the nodes' own are finite
     out, _ = p.call(check_status=True)
     assert (out[..., ::2] == float("inf")).all() and (out[..., 1::2] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,Hq,L", [(4, 4, 12), (7, 8, 40), (40, 32, 64)])
+def test_weights_over_f16_pools_keep_more_than_one_f16_value(D, T, Hq, L):
+    """Logits near one another, so that a logit's own error is small: with weights of one f16 value (off by up to 2^-12) the
+    outputs miss the bound, as a pair of f16 (off by up to 2^-22, or 2^-32 of the largest) they hold it."""
+    p = Problem(70, kv="f16", q="f16", S=3, T=T, Hq=Hq, Hkv=2, D=D, L=L, amp=0.05)
+    assert_near(*p.call(), p.want(), D, 20, T, 1.0)
