@@ -33,8 +33,8 @@
 //   codes      arrive in a ring of their own, their scales beside them
 //   wideners   eight warps turn a tile's codes into 16-bit values in the products' layout: K in Q's type, V in f16,
 //              exact in both (|code| <= 127, and every E4M3 value is an f16 and a bf16 value)
-//   scales     the K scale multiplies the logit, the V scale the weight, which is then rounded once to f16.  The references
-//              stand 2^E higher, 2^E being above every V scale of the unit's tiles so far, so weights stay within
+//   scales     the K scale multiplies the logit, the V scale the weight, which is then rounded once to f16 (11 bits, as in
+//              quantised decode: the wideners set the pace, and issue slots are scarce).  The references stand 2^E higher, 2^E being above every V scale of the unit's tiles so far, so weights stay within
 //              f16's range; those of entries whose scale is within 2^-21 of the largest keep all 11 bits.
 //
 // Entries hidden by the tree have weight 0, but 0 * V is NaN where V is not finite.  Such values of nodes are
@@ -205,7 +205,7 @@ __device__ __forceinline__ uint32_t odd_columns(const TreeParams& p, const int32
   }
   return __reduce_or_sync(0xffffffffu, found);
 }
-// 32 logits of a chunk: y = S * scale (quantised pools), hidden ones -inf.
+// 32 logits of a chunk: y = S * scale (quantised pools).
 __device__ __forceinline__ void scale32(uint32_t (&sv)[32], const float* ksc) {
 #pragma unroll
   for (int k = 0; k < 32; k += 4) {
@@ -747,8 +747,7 @@ __global__ void __launch_bounds__(TreeShape<D, KIND>::NWARP * 32, 1)
       for (int j = start; j < n; j += step, ++done) {
         const int jb = (t_lo + j) * BN;   // list position of the tile's first entry
         uint32_t bits[2];
-        // rows without a node take part unmasked (their sums are dropped): a warp goes the masked way
-        // for hidden entries alone
+        // a row without a node has an empty line: in tiles with nodes it sees the context alone (its sums are dropped)
         bool masked = false;
         const bool nodes_here = jb + BN > base;
 #pragma unroll
