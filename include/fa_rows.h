@@ -244,11 +244,19 @@ fa_status fa_rows_prefill_heads(const fa_rows_args* a, void* ws, size_t ws_bytes
  * lse = -inf.
  *   parent   [S, T] int32, n_nodes [S] int32 or NULL; T up to 256
  *   pools    every kind of fa_rows_args, D <= 256 with 16-byte multiples per
- *            (row, KV head); S * Hkv * T * Hq / Hkv * L / 1024 must fit int32
+ *            (row, KV head); S * Hkv * T * Hq / Hkv * L / 1024 must fit int32.
+ *            Tensor cores: D 64, 128 and 256 of 16-bit pools and D 128 of
+ *            quantised ones, with Hq / Hkv up to 128 and q 16-byte aligned.  Every
+ *            other call runs on the CUDA cores, tens of times slower: INT8, INT4
+ *            and E4M3 at D 64 and 256, other D, larger groups, unaligned q
  *   ws       fa_rows_tree_workspace_size bytes, 256-byte aligned, zero-filled
  *            once; one workspace may serve this call and fa_rows_decode in turn
  * The lists are cut into equal shares for all SMs whatever their lengths; two
- * launches.  Equal calls give equal bits.
+ * launches.  Equal calls give equal bits.  On the tensor cores a weight is a pair
+ * of 16-bit values over 16-bit pools, and over quantised ones, times its V scale,
+ * one f16 value (off by up to 2^-12).  Values that are not finite reach the
+ * nodes that see them alone: an infinite V gives an infinity, a NaN, or
+ * infinities of both signs, a NaN.
  */
 size_t fa_rows_tree_workspace_size(const fa_rows_args* a);
 fa_status fa_rows_tree(const fa_rows_args* a, const int32_t* parent, const int32_t* n_nodes, void* ws, size_t ws_bytes,

@@ -20,8 +20,8 @@
 // Measured on 16 sequences of 2k to 32k tokens in pages, 32/8 heads, 64 nodes (bf16, 768 MB): tiles of 128, one S a group
 // and one issuer of one lane 313 us; tiles of 64 with two S 398, the issuer busy throughout; two issuers 324; converged
 // warps 259; barriers that a poll has seen not waited for again, and asked side by side, 254; warps without a node idle,
-// 249 (3.1 TB/s); one product for both S of a group 293, since it waits for both.  An f16 pool 256.  INT8 codes, 24 nodes
-// (389 MB): 167.  4 x 16,384 shuffled bf16 rows, 16 nodes (270 MB): 76 (3.6 TB/s).
+// 249 to 252 (3.0 TB/s); one product for both S of a group 293, since it waits for both.  An f16 pool 256.  Codes, 24
+// nodes: INT8 (389 MB) 166, INT4 175, E4M3 235.  4 x 16,384 shuffled bf16 rows, 16 nodes (270 MB): 75 (3.6 TB/s).
 //
 // The softmax keeps a reference per row that moves only when the maximum has grown by
 // more than 2^8 (then O is rescaled in tensor memory); over 16-bit pools P goes over S as the pair rn(P), rn(P - rn(P)) of
