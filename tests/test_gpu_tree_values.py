@@ -43,7 +43,8 @@ def test_a_nan_in_one_nodes_v_reaches_exactly_those_that_see_it(kv, q, S, T, Hq,
         assert same_but_nan(out, want)
 
 
-@pytest.mark.parametrize("kv,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 64), ("f16", 128), ("f16", 256)])
+@pytest.mark.parametrize("kv,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f16", 64), ("f16", 128), ("f16", 256),
+                                  ("bf16", 96), ("f16", 40)])
 @pytest.mark.parametrize("T,Hq,L,spread", [(5, 8, 150, 1.0), (40, 32, 700, 1.0), (12, 8, 9000, 1.0), (5, 8, 190, 12.0)])
 def test_infinities_of_the_context_come_out_as_infinities(kv, D, T, Hq, L, spread):
     """Every node sees them with a weight above 0: an infinity where all of a component have one sign, else NaN.  spread: the
