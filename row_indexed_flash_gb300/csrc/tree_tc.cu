@@ -34,8 +34,9 @@
 //   wideners   eight warps turn a tile's codes into 16-bit values in the products' layout: K in Q's type, V in f16,
 //              exact in both (|code| <= 127, and every E4M3 value is an f16 and a bf16 value)
 //   scales     the K scale multiplies the logit, the V scale the weight, which is then rounded once to f16 (11 bits, as in
-//              quantised decode: the wideners set the pace, and issue slots are scarce).  The references stand 2^E higher, 2^E being above every V scale of the unit's tiles so far, so weights stay within
-//              f16's range; those of entries whose scale is within 2^-21 of the largest keep all 11 bits.
+//              quantised decode; a pair would cost 14 % over INT8, whose issue slots are scarce).  The references stand
+//              2^E higher, 2^E being above every V scale of the unit's tiles so far, so weights stay within f16's range;
+//              those of entries whose scale is within 2^-21 of the largest keep all 11 bits.
 //
 // Entries hidden by the tree have weight 0, but 0 * V is NaN where V is not finite.  Such values of nodes are
 // therefore taken out of the staged V (by the softmax warps, of E4M3 codes by the wideners), and the rows that do see their

@@ -1,4 +1,4 @@
-"""Attention of drafted trees (fa_rows_tree) over values that are not finite, where calls have many short units of work."""
+"""Attention of drafted trees (fa_rows_tree): values that are not finite, many short lists, the precision of weights."""
 import pytest
 import torch
 
